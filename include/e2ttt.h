@@ -268,6 +268,122 @@ e2ttt_status e2ttt_chunk_scan_bwd(const e2ttt_shape* shape,
                                   void* workspace, size_t workspace_bytes,
                                   void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around a recurrent layer. They share the conventions above (no
+ * allocation, asynchronous on `stream`, host-side checks with nothing written
+ * on a refusal, outputs disjoint from inputs and from each other except where
+ * "in place" is said, deterministic results) and the layouts: heads before
+ * tokens, tokens before channels, row-major and contiguous. Pointers need the
+ * alignment of their elements; 16-byte aligned ones are read in vectors.
+ *
+ * lengths (int32 [B] on the device, may be NULL): the number of tokens that each
+ * batch row of a padded batch has; values outside [0, T] are taken as the nearer
+ * bound. Tokens from lengths[b] on are never read as values (they may hold
+ * anything, NaN included); their rows of every per-token output are written as
+ * zeros, and end states are those after the row's last token (the start state,
+ * for a row of length 0).
+ */
+
+/* Short causal depthwise convolution over tokens, as it precedes a recurrent
+ * layer, for every (batch row, head, channel):
+ *   z_t = bias + sum_{j<W} w_j x_{t-(W-1)+j},   y_t = silu ? silu(z_t) : z_t
+ *   x [B, H, T, d] (act dtype), w [H, d, W] fp32, bias [H, d] fp32 or NULL
+ *   state [B, H, W-1, d] (act dtype) or NULL: the W-1 inputs before the first
+ *   token, oldest first; NULL stands for zeros.
+ * Limits: all sizes >= 1, W <= 8, B*H <= 65535, T <= 2^24, H*d*W < 2^31. */
+typedef struct {
+  int B, H, T, d, W;
+  int act;  /* e2ttt_dtype */
+  int silu; /* 0 or 1 */
+} e2ttt_conv_shape;
+
+/* Outputs: y [B, H, T, d] (act dtype); state_end [B, H, W-1, d] or NULL: the
+ * last W-1 inputs, those of `state` included where a row is shorter. */
+e2ttt_status e2ttt_short_conv_fwd(const e2ttt_conv_shape* shape, const void* x, const float* w,
+                                  const float* bias, const void* state, const int* lengths,
+                                  void* y, void* state_end, void* stream);
+
+/* Gradients of <dy, y> + <dstate_end, state_end>. dstate_end may be NULL (zero).
+ * Outputs: dx (act dtype), dw [H, d, W] fp32, dbias [H, d] fp32 or NULL, dstate
+ * [B, H, W-1, d] (act dtype) or NULL. workspace: at least
+ * e2ttt_short_conv_workspace_bytes(shape) bytes, 256-byte aligned. */
+size_t e2ttt_short_conv_workspace_bytes(const e2ttt_conv_shape* shape);
+e2ttt_status e2ttt_short_conv_bwd(const e2ttt_conv_shape* shape, const void* x, const float* w,
+                                  const float* bias, const void* state, const int* lengths,
+                                  const void* dy, const void* dstate_end, void* dx, float* dw,
+                                  float* dbias, void* dstate, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* One token per batch row (shape->T must be 1): x, y [B, H, d]; `state` is read
+ * and updated in place (NULL only where W = 1). */
+e2ttt_status e2ttt_short_conv_step(const e2ttt_conv_shape* shape, const void* x, const float* w,
+                                   const float* bias, void* state, void* y, void* stream);
+
+/* Selective state-space scan with one decay per head and token:
+ *   S_t = exp(dt_t A_h) S_{t-1} + dt_t v_t k_t^T,   y_t = S_t q_t + D_h v_t
+ *   v, y [B, H, T, d_v], q, k [B, G, T, d_k] (act dtype); heads
+ *   g*H/G .. (g+1)*H/G-1 share q and k of group g. (In state-space terms v is the
+ *   input, k the input matrix and q the output matrix of the token.)
+ *   dt [B, H, T] fp32 VALUES (after any softplus), A [H] fp32 (negative for a
+ *   decaying state), D [H] fp32 or NULL (no skip), S [B, H, d_v, d_k] fp32.
+ * States, decays and sums are held in fp32, the logarithms' sums in 64 bits. A
+ * NaN or infinity in a valid token may reach every token of its chunk (64
+ * tokens), earlier ones too, and all later ones.
+ * Limits: all sizes >= 1, H a multiple of G, d_k <= 256, d_v <= 1024,
+ * B*H <= 65535, T <= 2^24. */
+typedef struct {
+  int B, H, G, T;
+  int d_k, d_v;
+  int act; /* e2ttt_dtype */
+} e2ttt_ssm_shape;
+
+/* Bytes of scratch for the forward (for_bwd = 0) or backward (1), and of
+ * saved_states; 0 for an invalid shape. */
+size_t e2ttt_ssm_workspace_bytes(const e2ttt_ssm_shape* shape, int for_bwd);
+size_t e2ttt_ssm_saved_bytes(const e2ttt_ssm_shape* shape);
+
+/* Prompts. S0 may be NULL (zero). Outputs: y, S_end (the state after each row's
+ * last token) and saved_states (may be NULL; what the backward needs, opaque). */
+e2ttt_status e2ttt_ssm_scan_fwd(const e2ttt_ssm_shape* shape, const void* q, const void* k,
+                                const void* v, const float* dt, const float* A, const float* D,
+                                const float* S0, const int* lengths, void* y, float* S_end,
+                                float* saved_states, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Gradients of <dy, y> + <dS_end, S_end>, given the forward's inputs (lengths
+ * too) and its saved_states. dS_end may be NULL (zero). Outputs: dq, dk, dv (act
+ * dtype), ddt [B, H, T], dA [H], dD [H] (NULL exactly where D is) and dS0
+ * [B, H, d_v, d_k] (may be NULL), fp32. */
+e2ttt_status e2ttt_ssm_scan_bwd(const e2ttt_ssm_shape* shape, const void* q, const void* k,
+                                const void* v, const float* dt, const float* A, const float* D,
+                                const int* lengths, const float* saved_states, const void* dy,
+                                const float* dS_end, void* dq, void* dk, void* dv, float* ddt,
+                                float* dA, float* dD, float* dS0, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* One token per batch row (shape->T must be 1): q, k [B, G, d_k], v, y
+ * [B, H, d_v], dt [B, H]; S is updated in place. */
+e2ttt_status e2ttt_ssm_step(const e2ttt_ssm_shape* shape, const void* q, const void* k,
+                            const void* v, const float* dt, const float* A, const float* D,
+                            float* S, void* y, void* stream);
+
+/* Global 2-norm of `count` gradient tensors, and their clipping by it:
+ *   norm = sqrt(sum g^2) (one fp32 value on the device)
+ *   out  = g * min(1, max_norm / (norm + 1e-6))
+ * g, out: HOST arrays of `count` device pointers; n: HOST array of element counts
+ * (0 allowed, the pointer is then ignored); act: HOST array of e2ttt_dtype. out,
+ * or an entry of it, NULL or equal to g's: in place (nothing is written where the
+ * norm is within max_norm). Other outputs must not overlap any gradient. Tensors
+ * are contiguous; no two overlap. A NaN in any gradient makes the norm and every
+ * output NaN, an infinity makes the norm infinite and the finite outputs zero.
+ * workspace: e2ttt_grad_workspace_bytes(count) bytes, 256-byte aligned. */
+size_t e2ttt_grad_workspace_bytes(int count);
+e2ttt_status e2ttt_grad_norm(const void* const* g, const size_t* n, const int* act, int count,
+                             float* norm, void* workspace, size_t workspace_bytes, void* stream);
+e2ttt_status e2ttt_clip_grad_norm(const void* const* g, void* const* out, const size_t* n,
+                                  const int* act, int count, float max_norm, float* norm,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Status of the device-side bounded waits of the last compute call that used
  * `workspace`: synchronizes `stream`, then returns E2TTT_ERR_TIMEOUT if a
  * tensor-core kernel gave up waiting (its outputs are then invalid; the CUDA

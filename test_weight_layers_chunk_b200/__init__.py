@@ -289,3 +289,26 @@ def chunk_scan_bwd(q, k, v, lr, mom, decay, saved_states, dout, dW_end=None, dM_
                          g["dq"], g["dk"], g["dv"], g["dlr"], g["dmom"], g["ddecay"], g["dW0"],
                          g["dM0"], ws, stream=stream)
     return g
+
+
+# Operators around a recurrent layer (loads torch, as its tensors are checked there).
+_SEQUENCE = ("make_conv_shape", "make_ssm_shape", "short_conv_fwd", "short_conv_bwd",
+             "short_conv_step", "ssm_scan_fwd", "ssm_scan_bwd", "ssm_step", "grad_norm",
+             "clip_grad_norm", "e2ttt_conv_shape", "e2ttt_ssm_shape",
+             "e2ttt_short_conv_workspace_bytes", "e2ttt_short_conv_fwd", "e2ttt_short_conv_bwd",
+             "e2ttt_short_conv_step", "e2ttt_ssm_workspace_bytes", "e2ttt_ssm_saved_bytes",
+             "e2ttt_ssm_scan_fwd", "e2ttt_ssm_scan_bwd", "e2ttt_ssm_step",
+             "e2ttt_grad_workspace_bytes", "e2ttt_grad_norm", "e2ttt_clip_grad_norm")
+
+
+def __getattr__(name):
+    if name in _SEQUENCE:
+        from . import sequence
+        for n in _SEQUENCE:
+            globals()[n] = getattr(sequence, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_SEQUENCE))

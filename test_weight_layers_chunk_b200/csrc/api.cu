@@ -176,7 +176,13 @@ bool check_overlaps(const Range* in, int nin, const Range* out, int nout, std::s
 
 // Lets other translation units of the library report a failure through
 // e2ttt_last_error().
-void set_last_error(const char* msg) { g_last_error = msg; }
+void set_last_error(const char* msg) {
+  try {
+    g_last_error = msg;
+  } catch (...) {  // no exception leaves a C entry point
+    g_last_error.clear();
+  }
+}
 
 }  // namespace e2ttt
 

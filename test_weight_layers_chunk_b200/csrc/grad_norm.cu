@@ -1,0 +1,268 @@
+// Global 2-norm of many gradient tensors and their clipping by it:
+//   norm = sqrt(sum over tensors and elements of g^2),
+//   out  = g min(1, max_norm / (norm + 1e-6)).
+//
+// Bound by HBM: the norm reads every gradient once; the clip reads them again
+// and writes them, and reads nothing where the norm is within max_norm and the
+// clip is in place. The tensors are cut into pieces of kPiece elements; block i
+// takes the pieces i, i + grid, ... of the whole list, so one launch serves
+// many small tensors as well as a few large ones (the list travels as a kernel
+// parameter, kMany tensors to a launch). Squares are summed in fp32 over one
+// 16-byte vector, then in fp64, to one partial per block; the clip's blocks each
+// add up all partials themselves, in the same order, so no block waits for
+// another and results repeat bit for bit.
+#include "seq_ops.h"
+#include "trace.h"
+
+namespace e2ttt {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPiece = 8192;
+constexpr int kFew = 32, kMany = 480;
+
+struct Item {
+  const void* g;
+  void* out;
+  unsigned long long n;
+  unsigned first;  // its first piece in the launch's list
+  unsigned act;    // 1: bf16
+};
+template <int MAX>
+struct List {
+  Item t[MAX];
+  int count;
+  unsigned pieces;
+};
+
+// The tensor that piece `p` belongs to (first <= p, the last such one).
+template <int MAX>
+__device__ __forceinline__ int find(const List<MAX>& l, unsigned p) {
+  int lo = 0, hi = l.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (l.t[mid].first <= p) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <typename T> struct Wide { static constexpr int N = 16 / sizeof(T); };
+
+// Sum of squares of one vector. In fp32 while that neither overflows nor loses
+// small values; else each square in fp64.
+template <typename T>
+__device__ __forceinline__ double squares(const uint4& raw) {
+  const T* p = reinterpret_cast<const T*>(&raw);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < Wide<T>::N; ++i) s = fmaf(to_f<T>(p[i]), to_f<T>(p[i]), s);
+  if (s > 1e-24f && s < 1e37f) return s;
+  double a = 0.0;
+#pragma unroll
+  for (int i = 0; i < Wide<T>::N; ++i) a += (double)to_f<T>(p[i]) * to_f<T>(p[i]);
+  return a;
+}
+template <typename T>
+__device__ __forceinline__ double square1(T v) {
+  const double x = to_f<T>(v);
+  return x * x;
+}
+
+template <typename T>
+__device__ double piece_squares(const Item& it, unsigned piece) {
+  constexpr int N = Wide<T>::N;
+  const unsigned long long beg = (unsigned long long)piece * kPiece;
+  const int n = (int)(it.n - beg < kPiece ? it.n - beg : kPiece);
+  const T* g = (const T*)it.g + beg;
+  double a = 0.0;
+  // elements before the first 16-byte boundary, whole vectors, the rest
+  const int head = min(n, (int)(((16 - ((uintptr_t)g & 15)) & 15) / sizeof(T)));
+  const int nv = (n - head) / N;
+  const uint4* v = reinterpret_cast<const uint4*>(g + head);
+  if ((int)threadIdx.x < head) a += square1<T>(g[threadIdx.x]);
+  constexpr int U = 4;
+  for (int i = threadIdx.x; i < nv; i += kThreads * U) {
+    uint4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = i + u * kThreads < nv ? v[i + u * kThreads] : uint4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < U; ++u) a += squares<T>(r[u]);
+  }
+  for (int i = head + nv * N + threadIdx.x; i < n; i += kThreads) a += square1<T>(g[i]);
+  return a;
+}
+
+// Sum over the block, to every thread, in a fixed order.
+__device__ __forceinline__ double block_sum(double a) {
+  __shared__ double s[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = a;
+  __syncthreads();
+  a = 0.0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) a += s[i];
+  return a;
+}
+
+__device__ __forceinline__ double partials_sum(const double* part, int n) {
+  double a = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) a += part[i];
+  return block_sum(a);
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads)
+    grad_squares_kernel(const __grid_constant__ List<MAX> l, double* __restrict__ part) {
+  double a = 0.0;
+  for (unsigned p = blockIdx.x; p < l.pieces; p += gridDim.x) {
+    const Item& it = l.t[find(l, p)];
+    a += it.act ? piece_squares<bf16>(it, p - it.first) : piece_squares<float>(it, p - it.first);
+  }
+  a = block_sum(a);
+  if (threadIdx.x == 0) part[blockIdx.x] = a;
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* __restrict__ part, int n,
+                                                             float* __restrict__ norm) {
+  const double s = partials_sum(part, n);
+  if (threadIdx.x == 0) *norm = (float)sqrt(s);
+}
+
+template <typename T>
+__device__ void piece_scale(const Item& it, unsigned piece, float scale) {
+  constexpr int N = Wide<T>::N;
+  const unsigned long long beg = (unsigned long long)piece * kPiece;
+  const int n = (int)(it.n - beg < kPiece ? it.n - beg : kPiece);
+  const T* g = (const T*)it.g + beg;
+  T* o = (T*)it.out + beg;
+  const bool same = (((uintptr_t)g ^ (uintptr_t)o) & 15) == 0;
+  const int head = same ? min(n, (int)(((16 - ((uintptr_t)g & 15)) & 15) / sizeof(T))) : n;
+  const int nv = (n - head) / N;
+  for (int i = threadIdx.x; i < head; i += kThreads) o[i] = from_f<T>(to_f<T>(g[i]) * scale);
+  const uint4* v = reinterpret_cast<const uint4*>(g + head);
+  uint4* w = reinterpret_cast<uint4*>(o + head);
+  constexpr int U = 4;
+  for (int i = threadIdx.x; i < nv; i += kThreads * U) {
+    uint4 r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * kThreads < nv) r[u] = v[i + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      T* p = reinterpret_cast<T*>(&r[u]);
+#pragma unroll
+      for (int e = 0; e < N; ++e) p[e] = from_f<T>(to_f<T>(p[e]) * scale);
+      if (i + u * kThreads < nv) w[i + u * kThreads] = r[u];
+    }
+  }
+  for (int i = head + nv * N + threadIdx.x; i < n; i += kThreads)
+    o[i] = from_f<T>(to_f<T>(g[i]) * scale);
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads)
+    grad_clip_kernel(const __grid_constant__ List<MAX> l, const double* __restrict__ part, int n,
+                     float max_norm, float* __restrict__ norm) {
+  const float total = (float)sqrt(partials_sum(part, n));
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  const float c = max_norm / (total + 1e-6f);
+  const float scale = c > 1.f ? 1.f : c;  // a NaN norm scales by NaN
+  // Last piece first: what the norm's pass read last is still in L2.
+  for (unsigned q = blockIdx.x; q < l.pieces; q += gridDim.x) {
+    const unsigned p = l.pieces - 1 - q;
+    const Item& it = l.t[find(l, p)];
+    if (scale == 1.f && it.g == it.out) continue;
+    if (it.act)
+      piece_scale<bf16>(it, p - it.first, scale);
+    else
+      piece_scale<float>(it, p - it.first, scale);
+  }
+}
+
+// Fills `l` with up to MAX non-empty tensors from index `at` on; returns the
+// index after the last one taken.
+template <int MAX>
+int take(const GradList& g, int at, List<MAX>* l) {
+  l->count = 0;
+  l->pieces = 0;
+  for (; at < g.count && l->count < MAX; ++at) {
+    if (!g.n[at]) continue;
+    const unsigned long long pieces = (g.n[at] + kPiece - 1) / kPiece;
+    if (l->count && pieces + l->pieces > 0x7fffffffull) break;
+    l->t[l->count++] = Item{g.g[at], g.out && g.out[at] ? g.out[at] : const_cast<void*>(g.g[at]),
+                            (unsigned long long)g.n[at], l->pieces, (unsigned)(g.act[at] == 1)};
+    l->pieces += (unsigned)pieces;
+  }
+  return at;
+}
+
+template <int MAX>
+cudaError_t squares_t(const GradList& g, double* part, int* parts, cudaStream_t st) {
+  List<MAX> l;
+  *parts = 0;
+  for (int at = 0; at < g.count;) {
+    at = take(g, at, &l);
+    if (!l.count) break;
+    int blocks = sm_count() * 4;
+    if (blocks > kGradBlocksMax) blocks = kGradBlocksMax;
+    if ((unsigned)blocks > l.pieces) blocks = (int)l.pieces;
+    E2TTT_TRACE("grad_squares", st);
+    grad_squares_kernel<MAX><<<blocks, kThreads, 0, st>>>(l, part + *parts);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    *parts += blocks;
+  }
+  return cudaSuccess;
+}
+
+template <int MAX>
+cudaError_t clip_t(const GradList& g, const double* part, int parts, float max_norm, float* norm,
+                   cudaStream_t st) {
+  List<MAX> l;
+  for (int at = 0; at < g.count;) {
+    at = take(g, at, &l);
+    if (!l.count) break;
+    int blocks = sm_count() * 4;
+    if ((unsigned)blocks > l.pieces) blocks = (int)l.pieces;
+    E2TTT_TRACE("grad_clip", st);
+    grad_clip_kernel<MAX><<<blocks, kThreads, 0, st>>>(l, part, parts, max_norm, norm);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    norm = nullptr;  // the first launch writes it
+  }
+  return cudaSuccess;
+}
+
+cudaError_t squares_of(const GradList& g, double* part, int* parts, cudaStream_t st) {
+  return g.count <= kFew ? squares_t<kFew>(g, part, parts, st) : squares_t<kMany>(g, part, parts, st);
+}
+
+}  // namespace
+
+size_t grad_workspace_bytes(int count) {
+  return (size_t)((count + kMany - 1) / kMany + 1) * kGradBlocksMax * sizeof(double);
+}
+
+cudaError_t grad_norm(const GradList& g, float* norm, void* ws, cudaStream_t st) {
+  int parts = 0;
+  const cudaError_t e = squares_of(g, (double*)ws, &parts, st);
+  if (e != cudaSuccess) return e;
+  E2TTT_TRACE("grad_norm", st);
+  grad_norm_kernel<<<1, kThreads, 0, st>>>((const double*)ws, parts, norm);
+  return cudaGetLastError();
+}
+
+cudaError_t grad_clip(const GradList& g, float max_norm, float* norm, void* ws, cudaStream_t st) {
+  int parts = 0;
+  bool any = false;
+  for (int i = 0; i < g.count; ++i) any = any || g.n[i];
+  if (!any) return grad_norm(g, norm, ws, st);
+  const cudaError_t e = squares_of(g, (double*)ws, &parts, st);
+  if (e != cudaSuccess) return e;
+  return g.count <= kFew ? clip_t<kFew>(g, (const double*)ws, parts, max_norm, norm, st)
+                         : clip_t<kMany>(g, (const double*)ws, parts, max_norm, norm, st);
+}
+
+}  // namespace e2ttt

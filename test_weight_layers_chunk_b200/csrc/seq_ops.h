@@ -1,0 +1,98 @@
+// Internal interfaces of the operators around a recurrent layer: the short
+// causal convolution (conv.cu), the state-space scan (ssm.cu, ssm_tc.cu) and
+// the gradient norm (grad_norm.cu). Their C entry points are in seq_api.cu.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace e2ttt {
+
+// Number of SMs of the current device (asked once per device and thread).
+int sm_count();
+
+// ------------------------------------------------------------------ convolution
+struct ConvDims {
+  int B, H, T, d, W;
+  bool bf16_act, silu;
+};
+struct ConvArgs {
+  ConvDims s;
+  const void* x;
+  const float *w, *bias;  // bias may be NULL
+  const void* state;      // may be NULL: zeros
+  const int* lengths;     // may be NULL: T everywhere
+  bool vec;               // 16-byte vectors apply: row size and every pointer
+  cudaStream_t st;
+};
+size_t conv_bwd_workspace_bytes(const ConvDims& s);
+cudaError_t conv_fwd(const ConvArgs& a, void* y, void* state_end);
+cudaError_t conv_bwd(const ConvArgs& a, const void* dy, const void* dstate_end, void* dx, float* dw,
+                     float* dbias, void* dstate, void* ws);
+cudaError_t conv_step(const ConvArgs& a, void* state, void* y);
+
+// ------------------------------------------------------------------ scan
+struct SsmDims {
+  int B, H, G, T;
+  int N, P;      // state columns (d_k) and rows (d_v)
+  int Q, NC;     // tokens per chunk, chunks
+  int NPT;       // tiles of kSsmPT state rows
+  bool bf16_act;
+};
+constexpr int kSsmPT = 64;
+
+struct SsmFwdArgs {
+  SsmDims s;
+  const void *q, *k, *v;
+  const float *dt, *A, *D, *S0;
+  const int* lengths;
+  void* y;
+  float* S_end;
+  float* states;  // [NC][B*H][P][N]: saved_states or workspace
+  float* decay;   // [NC][B*H] workspace
+  cudaStream_t st;
+};
+cudaError_t ssm_fwd(const SsmFwdArgs& a);
+
+struct SsmBwdArgs {
+  SsmDims s;
+  const void *q, *k, *v;
+  const float *dt, *A, *D;
+  const int* lengths;
+  const float* states;  // from the forward
+  const void* dy;
+  const float* dS_end;
+  void *dq, *dk, *dv;
+  float *ddt, *dA, *dD, *dS0;
+  void* ws;
+  cudaStream_t st;
+};
+size_t ssm_bwd_workspace_bytes(const SsmDims& s);
+cudaError_t ssm_bwd(const SsmBwdArgs& a);
+
+struct SsmStepArgs {
+  SsmDims s;
+  const void *q, *k, *v;
+  const float *dt, *A, *D;
+  float* S;
+  void* y;
+  cudaStream_t st;
+};
+cudaError_t ssm_step(const SsmStepArgs& a);
+
+// ------------------------------------------------------------------ gradient norm
+struct GradList {
+  const void* const* g;
+  void* const* out;  // NULL: in place
+  const size_t* n;
+  const int* act;
+  int count;
+};
+constexpr int kGradBlocksMax = 1024;
+size_t grad_workspace_bytes(int count);
+cudaError_t grad_norm(const GradList& l, float* norm, void* ws, cudaStream_t st);
+cudaError_t grad_clip(const GradList& l, float max_norm, float* norm, void* ws, cudaStream_t st);
+
+}  // namespace e2ttt

@@ -1,0 +1,653 @@
+// State-space scan, fp32 CUDA-core kernels for every size and type, and the
+// passes over chunk states that all forms share. The mathematics is in ssm.cuh.
+//
+// A chunk's work is a handful of small matrix products, done here from shared
+// memory by 16 x 16 threads with 4 x 4 results each; chunks meet only in their
+// states, which one elementwise pass carries along the tokens.
+#include "ssm.cuh"
+#include "trace.h"
+
+namespace e2ttt {
+namespace {
+
+constexpr int kT = 256;
+
+// acc[i][j] += sum_k A(m_i, k) B(k, n_j), m_i = ty + 16 i, n_j = n0 + tx + 16 j
+// clamped to nmax. A at a + m*am + k*ak, B at b + k*bk + n*bn.
+template <int R>
+__device__ __forceinline__ void tile_mm(float (&acc)[R][4], const float* a, int am, int ak,
+                                        const float* b, int bk, int bn, int K, int n0, int nmax) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  int no[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) no[j] = min(n0 + tx + 16 * j, nmax) * bn;
+  for (int k = 0; k < K; ++k) {
+    float x[R], y[4];
+#pragma unroll
+    for (int i = 0; i < R; ++i) x[i] = a[(ty + 16 * i) * am + k * ak];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = b[k * bk + no[j]];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+  }
+}
+template <int R>
+__device__ __forceinline__ void clear(float (&acc)[R][4]) {
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+}
+// Sum over the 16 threads that share ty.
+__device__ __forceinline__ float row_sum16(float x) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
+}
+
+// rows x cols of src (row pitch `ld`) to dst (row pitch `pitch`), as fp32; rows
+// from n on and columns from cols to cpad are zero.
+template <typename T>
+__device__ __forceinline__ void load_tile(float* dst, int pitch, const T* src, long long ld, int rows,
+                                          int n, int cols, int cpad) {
+  for (int i = threadIdx.x; i < rows * cpad; i += kT) {
+    const int r = i / cpad, c = i - r * cpad;
+    dst[r * pitch + c] = r < n && c < cols ? to_f<T>(src[(long long)r * ld + c]) : 0.f;
+  }
+}
+
+struct Where {
+  int b, h, g, pt, c, bh, t0, n, p0, np;
+};
+__device__ __forceinline__ Where where(const SsmDims& s, const int* lengths) {
+  Where w;
+  w.bh = blockIdx.y;
+  w.b = w.bh / s.H;
+  w.h = w.bh - w.b * s.H;
+  w.g = w.h / (s.H / s.G);
+  w.c = blockIdx.x;
+  w.pt = blockIdx.z;
+  w.t0 = w.c * s.Q;
+  w.n = min(max(ssm_row_length(lengths, w.b, s.T) - w.t0, 0), s.Q);
+  w.p0 = w.pt * kSsmPT;
+  w.np = min(kSsmPT, s.P - w.p0);
+  return w;
+}
+
+__device__ __forceinline__ ChunkLogs chunk_logs(float* p, int Q) {
+  ChunkLogs L;
+  L.hi = p;
+  L.lo = p + Q;
+  L.eta = p + 2 * Q;
+  L.Q1 = Q - 1;
+  return L;
+}
+
+// states[c][bh] = the chunk's own contribution to its end state
+//   REV 0: sum_s e^{c_Q-c_s} eta_s x_s y_s^T  (x = v, y = k)
+//   REV 1: sum_t e^{c_t} x_t y_t^T            (x = dy, y = q; the adjoint)
+// and decay[c][bh] = e^{c_Q}.
+template <typename T, int REV>
+__global__ void __launch_bounds__(kT)
+    chunk_state_kernel(SsmDims s, const T* __restrict__ x, const T* __restrict__ y,
+                       const float* __restrict__ dt, const float* __restrict__ A,
+                       const int* __restrict__ lengths, float* __restrict__ states,
+                       float* __restrict__ decay) {
+  extern __shared__ float sm[];
+  const Where w = where(s, lengths);
+  const int Q = s.Q, N = s.N, XP = kSsmPT + 1, NP = N + 1;
+  const ChunkLogs L = chunk_logs(sm, Q);
+  float* xs = sm + 3 * Q;
+  float* ys = xs + Q * XP;
+  if (threadIdx.x < 32) fill_chunk_logs(L, dt + (long long)w.bh * s.T + w.t0, A[w.h], w.n);
+  load_tile<T>(ys, NP, y + (((long long)w.b * s.G + w.g) * s.T + w.t0) * N, N, Q, w.n, N, N);
+  load_tile<T>(xs, XP, x + ((long long)w.bh * s.T + w.t0) * s.P + w.p0, s.P, Q, w.n, w.np, kSsmPT);
+  __syncthreads();
+  for (int i = threadIdx.x; i < Q * kSsmPT; i += kT) {
+    const int t = i / kSsmPT, p = i - t * kSsmPT;
+    xs[t * XP + p] *= REV ? L.from_start(t) : L.to_end(t) * L.eta[t];
+  }
+  if (threadIdx.x == 0 && w.pt == 0)
+    decay[(long long)w.c * s.B * s.H + w.bh] = L.from_start(Q - 1);
+  __syncthreads();
+  float* out = states + (((long long)w.c * s.B * s.H + w.bh) * s.P + w.p0) * N;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  for (int n0 = 0; n0 < N; n0 += 64) {
+    float acc[4][4];
+    clear(acc);
+    tile_mm<4>(acc, xs, 1, XP, ys, NP, 1, Q, n0, N - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = ty + 16 * i, n = n0 + tx + 16 * j;
+        if (p < w.np && n < N) out[(long long)p * N + n] = acc[i][j];
+      }
+  }
+}
+
+// Turns the chunks' own contributions into the states at their starts (REV 0,
+// from `first`) or the gradients at their ends (REV 1, from the last chunk
+// back); `last` gets what is left after the last one.
+template <int REV>
+__global__ void __launch_bounds__(kT)
+    carry_kernel(int NC, int BH, long long PN, const float* __restrict__ first,
+                 const float* __restrict__ decay, float* __restrict__ states,
+                 float* __restrict__ last) {
+  const int bh = blockIdx.y;
+  const long long i = (long long)blockIdx.x * kT + threadIdx.x;
+  if (i >= PN) return;
+  float run = first ? first[bh * PN + i] : 0.f;
+  constexpr int U = 8;
+  for (int c0 = 0; c0 < NC; c0 += U) {
+    float own[U], d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
+      if (c0 + u < NC) {
+        own[u] = states[((long long)c * BH + bh) * PN + i];
+        d[u] = decay[(long long)c * BH + bh];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
+      if (c0 + u < NC) {
+        states[((long long)c * BH + bh) * PN + i] = run;
+        run = fmaf(d[u], run, own[u]);
+      }
+    }
+  }
+  if (last) last[bh * PN + i] = run;
+}
+
+// y of one chunk from the state at its start.
+template <typename T, int R>  // R = Q / 16
+__global__ void __launch_bounds__(kT)
+    chunk_out_kernel(SsmDims s, const T* __restrict__ q, const T* __restrict__ k,
+                     const T* __restrict__ v, const float* __restrict__ dt,
+                     const float* __restrict__ A, const float* __restrict__ D,
+                     const int* __restrict__ lengths, const float* __restrict__ states,
+                     T* __restrict__ y) {
+  extern __shared__ float sm[];
+  const Where w = where(s, lengths);
+  const int Q = s.Q, N = s.N, XP = kSsmPT + 1, NP = N + 1, QP = Q + 1;
+  const ChunkLogs L = chunk_logs(sm, Q);
+  float* qs = sm + 3 * Q;
+  float* ks = qs + Q * NP;  // then the state [PT][NP]
+  float* xs = ks + (Q > kSsmPT ? Q : kSsmPT) * NP;
+  float* ws = xs + Q * XP;
+  if (threadIdx.x < 32) fill_chunk_logs(L, dt + (long long)w.bh * s.T + w.t0, A[w.h], w.n);
+  const long long qo = (((long long)w.b * s.G + w.g) * s.T + w.t0) * N;
+  load_tile<T>(qs, NP, q + qo, N, Q, w.n, N, N);
+  load_tile<T>(ks, NP, k + qo, N, Q, w.n, N, N);
+  load_tile<T>(xs, XP, v + ((long long)w.bh * s.T + w.t0) * s.P + w.p0, s.P, Q, w.n, w.np, kSsmPT);
+  __syncthreads();
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float acc[R][4];
+  clear(acc);
+  tile_mm<R>(acc, qs, NP, 1, ks, 1, NP, N, 0, Q - 1);
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = ty + 16 * i, u = tx + 16 * j;
+      if (u < Q) ws[t * QP + u] = u <= t ? acc[i][j] * L.decay(t, u) * L.eta[u] : 0.f;
+    }
+  __syncthreads();
+  load_tile<float>(ks, NP, states + (((long long)w.c * s.B * s.H + w.bh) * s.P + w.p0) * N, N, kSsmPT,
+                   w.np, N, N);
+  __syncthreads();
+  clear(acc);
+  tile_mm<R>(acc, qs, NP, 1, ks, 1, NP, N, 0, kSsmPT - 1);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const float f = L.from_start(ty + 16 * i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] *= f;
+  }
+  tile_mm<R>(acc, ws, QP, 1, xs, XP, 1, Q, 0, kSsmPT - 1);
+  const float Dh = D ? D[w.h] : 0.f;
+  T* out = y + ((long long)w.bh * s.T + w.t0) * s.P + w.p0;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = ty + 16 * i, p = tx + 16 * j;
+      if (w.t0 + t < s.T && p < w.np)
+        out[(long long)t * s.P + p] =
+            from_f<T>(t < w.n ? fmaf(Dh, xs[t * XP + p], acc[i][j]) : 0.f);
+    }
+}
+
+// Sum over the block to thread 0, in a fixed order.
+__device__ __forceinline__ float block_sum0(float x, float* scratch) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0.f;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kT / 32; ++i) x += scratch[i];
+  return x;
+}
+
+// All gradients of one chunk from the state at its start and the gradient of the
+// state at its end. dq, dk per head and tile of state rows (fp32 partial sums
+// [B*H*NPT][T][N]), ddt per tile ([NPT][B*H][T]), dA and dD per chunk and tile
+// ([NC][NPT][B*H]).
+template <typename T, int R>
+__global__ void __launch_bounds__(kT)
+    chunk_grad_kernel(SsmDims s, const T* __restrict__ q, const T* __restrict__ k,
+                      const T* __restrict__ v, const float* __restrict__ dt,
+                      const float* __restrict__ A, const float* __restrict__ D,
+                      const int* __restrict__ lengths, const float* __restrict__ states,
+                      const float* __restrict__ ends, const T* __restrict__ dy,
+                      float* __restrict__ dqp, float* __restrict__ dkp, T* __restrict__ dv,
+                      float* __restrict__ ddtp, float* __restrict__ dAp, float* __restrict__ dDp) {
+  extern __shared__ float sm[];
+  const Where w = where(s, lengths);
+  const int Q = s.Q, N = s.N, XP = kSsmPT + 1, NP = N + 1, QP = Q + 1;
+  const ChunkLogs L = chunk_logs(sm, Q);
+  float* dots = sm + 3 * Q;  // [6][Q]: row sums, column sums, readers', sources', deta, K's diagonal
+  float* scratch = dots + 6 * Q;
+  float* qs = scratch + 16;
+  float* ks = qs + Q * NP;
+  float* Ss = ks + Q * NP;
+  float* Xs = Ss + kSsmPT * NP;
+  float* xs = Xs + kSsmPT * NP;
+  float* gs = xs + Q * XP;
+  float* Ws = gs + Q * XP;  // e^{c_t-c_s} (q_t.k_s)
+  float* Ks = Ws + Q * QP;  // e^{c_t-c_s} eta_s (dy_t.v_s)
+  float* cz = Ks + Q * QP;  // [2][16][Q]: column sums by thread row, of Z off its diagonal and of deta
+  if (threadIdx.x < 32) fill_chunk_logs(L, dt + (long long)w.bh * s.T + w.t0, A[w.h], w.n);
+  const long long qo = (((long long)w.b * s.G + w.g) * s.T + w.t0) * N;
+  const long long vo = ((long long)w.bh * s.T + w.t0) * s.P + w.p0;
+  const long long so = (((long long)w.c * s.B * s.H + w.bh) * s.P + w.p0) * N;
+  load_tile<T>(qs, NP, q + qo, N, Q, w.n, N, N);
+  load_tile<T>(ks, NP, k + qo, N, Q, w.n, N, N);
+  load_tile<T>(xs, XP, v + vo, s.P, Q, w.n, w.np, kSsmPT);
+  load_tile<T>(gs, XP, dy + vo, s.P, Q, w.n, w.np, kSsmPT);
+  load_tile<float>(Ss, NP, states + so, N, kSsmPT, w.np, N, N);
+  load_tile<float>(Xs, NP, ends + so, N, kSsmPT, w.np, N, N);
+  __syncthreads();
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  {
+    float m[R][4], kk[R][4];
+    clear(m);
+    clear(kk);
+    tile_mm<R>(m, qs, NP, 1, ks, 1, NP, N, 0, Q - 1);
+    tile_mm<R>(kk, gs, XP, 1, xs, 1, XP, kSsmPT, 0, Q - 1);
+    float colz[4] = {}, cold[4] = {};
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int t = ty + 16 * i;
+      float rows = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int u = tx + 16 * j;
+        if (u >= Q) continue;
+        const float e = u <= t ? L.decay(t, u) : 0.f;
+        const float a = u <= t ? e * m[i][j] : 0.f;
+        const float b = u <= t ? e * L.eta[u] * kk[i][j] : 0.f;
+        Ws[t * QP + u] = a;
+        Ks[t * QP + u] = b;
+        const float r = a * kk[i][j], z = u < t ? r * L.eta[u] : 0.f;
+        rows += z;
+        colz[j] += z;
+        cold[j] += r;
+        if (u == t) dots[5 * Q + t] = kk[i][j];
+      }
+      rows = row_sum16(rows);
+      if (tx == 0) dots[t] = rows;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int u = tx + 16 * j;
+      if (u >= Q) continue;
+      cz[ty * Q + u] = colz[j];
+      cz[(16 + ty) * Q + u] = cold[j];
+    }
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < Q; u += kT) {
+    float z = 0.f, de = 0.f;
+    for (int i = 0; i < 16; ++i) {
+      z += cz[i * Q + u];
+      de += cz[(16 + i) * Q + u];
+    }
+    dots[Q + u] = z;
+    dots[4 * Q + u] = de;
+  }
+  // dv
+  {
+    float acc[R][4];
+    clear(acc);
+    tile_mm<R>(acc, ks, NP, 1, Xs, 1, NP, N, 0, kSsmPT - 1);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float f = L.to_end(ty + 16 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] *= f;
+    }
+    tile_mm<R>(acc, Ws, 1, QP, gs, XP, 1, Q, 0, kSsmPT - 1);
+    const float Dh = D ? D[w.h] : 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = ty + 16 * i, p = tx + 16 * j;
+        if (w.t0 + t < s.T && p < w.np)
+          dv[vo + (long long)t * s.P + p] =
+              from_f<T>(t < w.n ? fmaf(L.eta[t], acc[i][j], Dh * gs[t * XP + p]) : 0.f);
+      }
+  }
+  // dq, dk and the dots of their state parts
+  const long long po = (((long long)w.bh * s.NPT + w.pt) * s.T + w.t0) * N;
+  float rd[R], sd[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) rd[i] = sd[i] = 0.f;
+  for (int n0 = 0; n0 < N; n0 += 64) {
+    float acc[R][4];
+    clear(acc);
+    tile_mm<R>(acc, gs, XP, 1, Ss, NP, 1, kSsmPT, n0, N - 1);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int t = ty + 16 * i;
+      const float f = L.from_start(t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + tx + 16 * j;
+        acc[i][j] *= f;
+        if (n < N) rd[i] = fmaf(acc[i][j], qs[t * NP + n], rd[i]);
+      }
+    }
+    tile_mm<R>(acc, Ks, QP, 1, ks, NP, 1, Q, n0, N - 1);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = ty + 16 * i, n = n0 + tx + 16 * j;
+        if (w.t0 + t < s.T && n < N) dqp[po + (long long)t * N + n] = t < w.n ? acc[i][j] : 0.f;
+      }
+    clear(acc);
+    tile_mm<R>(acc, xs, XP, 1, Xs, NP, 1, kSsmPT, n0, N - 1);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int t = ty + 16 * i;
+      const float f = L.to_end(t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + tx + 16 * j;
+        acc[i][j] *= f;
+        if (n < N) sd[i] = fmaf(acc[i][j], ks[t * NP + n], sd[i]);
+        acc[i][j] *= L.eta[t];
+      }
+    }
+    tile_mm<R>(acc, Ks, 1, QP, qs, NP, 1, Q, n0, N - 1);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = ty + 16 * i, n = n0 + tx + 16 * j;
+        if (w.t0 + t < s.T && n < N) dkp[po + (long long)t * N + n] = t < w.n ? acc[i][j] : 0.f;
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const float a = row_sum16(rd[i]), b = row_sum16(sd[i]);
+    if (tx == 0) {
+      dots[2 * Q + ty + 16 * i] = a;
+      dots[3 * Q + ty + 16 * i] = b;
+    }
+  }
+  // e^{c_Q} <S, X>
+  float ip = 0.f;
+  for (int i = threadIdx.x; i < kSsmPT * N; i += kT) {
+    const int p = i / N, n = i - p * N;
+    ip = fmaf(Ss[p * NP + n], Xs[p * NP + n], ip);
+  }
+  ip = block_sum0(ip, scratch);
+  if (threadIdx.x == 0) {
+    const float* rows = dots;
+    const float *cols = dots + Q, *rdr = dots + 2 * Q, *src = dots + 3 * Q, *de = dots + 4 * Q,
+                *kd = dots + 5 * Q;
+    const double through = (double)L.from_start(Q - 1) * ip;
+    double before = 0.0;  // sources before r, read after the chunk
+    for (int r = 0; r < Q; ++r) before += (double)L.eta[r] * src[r];
+    double after = 0.0, dA = 0.0, dD = 0.0;
+    const float Ah = A[w.h];
+    float* out = ddtp + ((long long)w.pt * s.B * s.H + w.bh) * s.T + w.t0;
+    for (int r = Q - 1; r >= 0; --r) {
+      before -= (double)L.eta[r] * src[r];
+      after += (double)rows[r] - cols[r] + rdr[r];
+      const double dl = after + before + through;
+      dA += L.eta[r] * dl;
+      dD += kd[r];
+      if (w.t0 + r < s.T) out[r] = r < w.n ? (float)(Ah * dl + de[r] + src[r]) : 0.f;
+    }
+    const long long o = ((long long)w.c * s.NPT + w.pt) * s.B * s.H + w.bh;
+    dAp[o] = (float)dA;
+    dDp[o] = (float)dD;
+  }
+}
+
+// out[b][g][i] = sum over the group's heads and their tiles of part, in order.
+template <typename T>
+__global__ void __launch_bounds__(kT)
+    group_sum_kernel(const float* __restrict__ part, int per, long long row, T* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * kT + threadIdx.x;
+  if (i >= row) return;
+  const float* p = part + (long long)blockIdx.y * per * row + i;
+  float a = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < per; ++j) a += p[(long long)j * row];
+  out[(long long)blockIdx.y * row + i] = from_f<T>(a);
+}
+
+__global__ void __launch_bounds__(kT) tile_sum_kernel(const float* __restrict__ part, int tiles,
+                                                      long long n, float* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * kT + threadIdx.x;
+  if (i >= n) return;
+  float a = 0.f;
+  for (int j = 0; j < tiles; ++j) a += part[(long long)j * n + i];
+  out[i] = a;
+}
+
+// dA[h], dD[h]: sums of part [rows][B][H], one block per head, in a fixed order.
+__global__ void __launch_bounds__(kT) head_sum_kernel(const float* __restrict__ dAp,
+                                                      const float* __restrict__ dDp, int rows, int H,
+                                                      float* __restrict__ dA,
+                                                      float* __restrict__ dD) {
+  __shared__ double s[kT];
+  const int h = blockIdx.x;
+  for (int which = 0; which < 2; ++which) {
+    const float* p = which ? dDp : dAp;
+    float* out = which ? dD : dA;
+    if (!out) continue;
+    double a = 0.0;
+    for (int i = threadIdx.x; i < rows; i += kT) a += p[(long long)i * H + h];
+    s[threadIdx.x] = a;
+    __syncthreads();
+    for (int o = kT / 2; o; o >>= 1) {
+      if (threadIdx.x < o) s[threadIdx.x] += s[threadIdx.x + o];
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) out[h] = (float)s[0];
+    __syncthreads();
+  }
+}
+
+// One token: S = e^{dt A} S + dt v k^T in place, y = S q + D v. Bound by HBM: S
+// is read and written once. Eight lanes share a state row, so a warp reads four
+// rows' 128-byte lines at a time.
+template <typename T>
+__global__ void __launch_bounds__(kT)
+    ssm_step_kernel(SsmDims s, const T* __restrict__ q, const T* __restrict__ k,
+                    const T* __restrict__ v, const float* __restrict__ dt,
+                    const float* __restrict__ A, const float* __restrict__ D,
+                    float* __restrict__ S, T* __restrict__ y) {
+  const int bh = blockIdx.y, b = bh / s.H, h = bh - b * s.H, g = h / (s.H / s.G);
+  const int p = blockIdx.x * (kT / 8) + threadIdx.x / 8, l = threadIdx.x & 7;
+  const bool on = p < s.P;
+  const float e = dt[bh], dec = ex2(e * A[h] * 1.44269504f);
+  const float x = on ? to_f<T>(v[(long long)bh * s.P + p]) : 0.f;
+  const T* qr = q + ((long long)b * s.G + g) * s.N;
+  const T* kr = k + ((long long)b * s.G + g) * s.N;
+  float* row = S + ((long long)bh * s.P + p) * s.N;
+  const float ex = e * x;
+  float acc = 0.f;
+  if (on)
+    for (int n = l; n < s.N; n += 8) {
+      const float u = fmaf(dec, row[n], ex * to_f<T>(kr[n]));
+      row[n] = u;
+      acc = fmaf(u, to_f<T>(qr[n]), acc);
+    }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
+  if (on && l == 0) y[(long long)bh * s.P + p] = from_f<T>(D ? fmaf(D[h], x, acc) : acc);
+}
+
+size_t state_smem(const SsmDims& s) {
+  return sizeof(float) * (3 * s.Q + (size_t)s.Q * (kSsmPT + 1) + (size_t)s.Q * (s.N + 1));
+}
+size_t out_smem(const SsmDims& s) {
+  return sizeof(float) * (3 * s.Q + (size_t)(s.Q + (s.Q > kSsmPT ? s.Q : kSsmPT)) * (s.N + 1) +
+                          (size_t)s.Q * (kSsmPT + 1) + (size_t)s.Q * (s.Q + 1));
+}
+size_t grad_smem(const SsmDims& s) {
+  return sizeof(float) * (9 * s.Q + 16 + (size_t)2 * (s.Q + kSsmPT) * (s.N + 1) +
+                          (size_t)2 * s.Q * (kSsmPT + 1) + (size_t)2 * s.Q * (s.Q + 1) +
+                          (size_t)32 * s.Q);
+}
+
+template <class F>
+cudaError_t allow_smem(F* f, size_t bytes) {
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct BwdWs {
+  size_t ends, decay, dqp, dkp, ddtp, dAp, dDp, total;
+};
+BwdWs bwd_layout(const SsmDims& s) {
+  BwdWs L{};
+  size_t o = 0;
+  const size_t f = sizeof(float), BH = (size_t)s.B * s.H;
+  auto take = [&](size_t n) { const size_t r = o; o = up256(o + n); return r; };
+  L.ends = take(s.NC * BH * s.P * s.N * f);
+  L.decay = take(s.NC * BH * f);
+  L.dqp = take(BH * s.NPT * s.T * s.N * f);
+  L.dkp = take(BH * s.NPT * s.T * s.N * f);
+  L.ddtp = take(s.NPT > 1 ? s.NPT * BH * s.T * f : 0);
+  L.dAp = take((size_t)s.NC * s.NPT * BH * f);
+  L.dDp = take((size_t)s.NC * s.NPT * BH * f);
+  L.total = o;
+  return L;
+}
+
+template <typename T>
+cudaError_t fwd_t(const SsmFwdArgs& a) {
+  const SsmDims& s = a.s;
+  const dim3 grid(s.NC, s.B * s.H, s.NPT);
+  const long long PN = (long long)s.P * s.N;
+  cudaError_t e;
+  {
+    E2TTT_TRACE("ssm_chunk_state", a.st);
+    if ((e = allow_smem(chunk_state_kernel<T, 0>, state_smem(s))) != cudaSuccess) return e;
+    chunk_state_kernel<T, 0><<<grid, kT, state_smem(s), a.st>>>(
+        s, (const T*)a.v, (const T*)a.k, a.dt, a.A, a.lengths, a.states, a.decay);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  {
+    E2TTT_TRACE("ssm_carry", a.st);
+    carry_kernel<0><<<dim3((unsigned)((PN + kT - 1) / kT), s.B * s.H), kT, 0, a.st>>>(
+        s.NC, s.B * s.H, PN, a.S0, a.decay, a.states, a.S_end);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  E2TTT_TRACE("ssm_chunk_out", a.st);
+  auto kern = s.Q == 64 ? chunk_out_kernel<T, 4> : chunk_out_kernel<T, 2>;
+  if ((e = allow_smem(kern, out_smem(s))) != cudaSuccess) return e;
+  kern<<<grid, kT, out_smem(s), a.st>>>(s, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.dt, a.A,
+                                        a.D, a.lengths, a.states, (T*)a.y);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t bwd_t(const SsmBwdArgs& a) {
+  const SsmDims& s = a.s;
+  const BwdWs L = bwd_layout(s);
+  char* w = (char*)a.ws;
+  float *ends = (float*)(w + L.ends), *decay = (float*)(w + L.decay), *dqp = (float*)(w + L.dqp),
+        *dkp = (float*)(w + L.dkp), *dAp = (float*)(w + L.dAp), *dDp = (float*)(w + L.dDp);
+  float* ddtp = s.NPT > 1 ? (float*)(w + L.ddtp) : a.ddt;
+  const int BH = s.B * s.H;
+  const dim3 grid(s.NC, BH, s.NPT);
+  const long long PN = (long long)s.P * s.N;
+  cudaError_t e;
+  {
+    E2TTT_TRACE("ssm_chunk_dstate", a.st);
+    if ((e = allow_smem(chunk_state_kernel<T, 1>, state_smem(s))) != cudaSuccess) return e;
+    chunk_state_kernel<T, 1><<<grid, kT, state_smem(s), a.st>>>(
+        s, (const T*)a.dy, (const T*)a.q, a.dt, a.A, a.lengths, ends, decay);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  {
+    E2TTT_TRACE("ssm_carry_back", a.st);
+    carry_kernel<1><<<dim3((unsigned)((PN + kT - 1) / kT), BH), kT, 0, a.st>>>(
+        s.NC, BH, PN, a.dS_end, decay, ends, a.dS0);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  {
+    E2TTT_TRACE("ssm_chunk_grad", a.st);
+    auto kern = s.Q == 64 ? chunk_grad_kernel<T, 4> : chunk_grad_kernel<T, 2>;
+    if ((e = allow_smem(kern, grad_smem(s))) != cudaSuccess) return e;
+    kern<<<grid, kT, grad_smem(s), a.st>>>(s, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.dt, a.A,
+                                           a.D, a.lengths, a.states, ends, (const T*)a.dy, dqp, dkp,
+                                           (T*)a.dv, ddtp, dAp, dDp);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const long long row = (long long)s.T * s.N;
+  const dim3 gsum((unsigned)((row + kT - 1) / kT), s.B * s.G);
+  {
+    E2TTT_TRACE("ssm_group_sum", a.st);
+    group_sum_kernel<T><<<gsum, kT, 0, a.st>>>(dqp, s.H / s.G * s.NPT, row, (T*)a.dq);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    group_sum_kernel<T><<<gsum, kT, 0, a.st>>>(dkp, s.H / s.G * s.NPT, row, (T*)a.dk);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (s.NPT > 1) {
+    const long long n = (long long)BH * s.T;
+    E2TTT_TRACE("ssm_tile_sum", a.st);
+    tile_sum_kernel<<<(unsigned)((n + kT - 1) / kT), kT, 0, a.st>>>(ddtp, s.NPT, n, a.ddt);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  E2TTT_TRACE("ssm_head_sum", a.st);
+  head_sum_kernel<<<s.H, kT, 0, a.st>>>(dAp, dDp, s.NC * s.NPT * s.B, s.H, a.dA, a.dD);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t ssm_bwd_workspace_bytes(const SsmDims& s) { return bwd_layout(s).total; }
+cudaError_t ssm_fwd(const SsmFwdArgs& a) { return a.s.bf16_act ? fwd_t<bf16>(a) : fwd_t<float>(a); }
+cudaError_t ssm_bwd(const SsmBwdArgs& a) { return a.s.bf16_act ? bwd_t<bf16>(a) : bwd_t<float>(a); }
+
+cudaError_t ssm_step(const SsmStepArgs& a) {
+  const SsmDims& s = a.s;
+  const dim3 grid((s.P + kT / 8 - 1) / (kT / 8), s.B * s.H);
+  E2TTT_TRACE("ssm_step", a.st);
+  if (s.bf16_act)
+    ssm_step_kernel<bf16><<<grid, kT, 0, a.st>>>(s, (const bf16*)a.q, (const bf16*)a.k,
+                                                 (const bf16*)a.v, a.dt, a.A, a.D, a.S, (bf16*)a.y);
+  else
+    ssm_step_kernel<float><<<grid, kT, 0, a.st>>>(s, (const float*)a.q, (const float*)a.k,
+                                                  (const float*)a.v, a.dt, a.A, a.D, a.S, (float*)a.y);
+  return cudaGetLastError();
+}
+
+}  // namespace e2ttt

@@ -327,8 +327,14 @@ e2ttt_status e2ttt_short_conv_step(const e2ttt_conv_shape* shape, const void* x,
  *   dt [B, H, T] fp32 VALUES (after any softplus), A [H] fp32 (negative for a
  *   decaying state), D [H] fp32 or NULL (no skip), S [B, H, d_v, d_k] fp32.
  * States, decays and sums are held in fp32, the logarithms' sums in 64 bits. A
- * NaN or infinity in a valid token may reach every token of its chunk (64
- * tokens), earlier ones too, and all later ones.
+ * NaN or infinity in a valid token may reach every token of its chunk (at most
+ * 128 tokens), earlier ones too, and all later ones.
+ * Paths: bf16 activations with d_k <= 128 run on the tcgen05 tensor cores
+ * (operands that are not inputs are rounded to bf16 where the result is bf16 and
+ * enter as three bf16 terms where it is fp32; fp32 accumulation), for any
+ * alignment and odd sizes; fp32 activations and larger d_k run on fp32 CUDA
+ * cores. The waits of the tensor-core kernels are bounded:
+ * e2ttt_workspace_status(workspace) reports one that gave up.
  * Limits: all sizes >= 1, H a multiple of G, d_k <= 256, d_v <= 1024,
  * B*H <= 65535, T <= 2^24. */
 typedef struct {

@@ -91,12 +91,13 @@ e2ttt_status ssm_dims(const char* who, const e2ttt_ssm_shape* s, SsmDims* d) {
   d->T = s->T;
   d->N = s->d_k;
   d->P = s->d_v;
-  // 64 tokens to a chunk; with more than 128 state columns the backward's tiles
-  // of 64 tokens would not fit an SM's shared memory.
-  d->Q = s->d_k <= 128 ? 64 : 32;
+  d->bf16_act = s->act == E2TTT_BF16;
+  d->tc = d->bf16_act && s->d_k <= 128;
+  // CUDA cores: 64 tokens to a chunk; with more than 128 state columns the
+  // backward's tiles of 64 tokens would not fit an SM's shared memory.
+  d->Q = d->tc ? kSsmTcChunk : s->d_k <= 128 ? 64 : 32;
   d->NC = (s->T + d->Q - 1) / d->Q;
   d->NPT = (s->d_v + kSsmPT - 1) / kSsmPT;
-  d->bf16_act = s->act == E2TTT_BF16;
   return E2TTT_OK;
 }
 
@@ -112,9 +113,18 @@ SsmBytes ssm_bytes(const SsmDims& d) {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Forward scratch: the chunks' decays, then their states (in saved_states where given).
-size_t ssm_fwd_bytes(const SsmDims& d) {
-  return up256((size_t)d.NC * d.B * d.H * 4) + up256(ssm_bytes(d).saved);
+// Forward scratch: status word, the chunks' decays, their logarithms (tensor
+// cores) and their states (in saved_states where given).
+struct SsmFwdWs {
+  size_t decay, logs, states, total;
+};
+SsmFwdWs ssm_fwd_layout(const SsmDims& d) {
+  SsmFwdWs L{};
+  L.decay = 256;
+  L.logs = L.decay + up256((size_t)d.NC * d.B * d.H * 4);
+  L.states = L.logs + (d.tc ? up256(ssm_tc_logs_bytes(d)) : 0);
+  L.total = L.states + up256(ssm_bytes(d).saved);
+  return L;
 }
 
 // ------------------------------------------------------------------ gradients
@@ -254,7 +264,7 @@ e2ttt_status e2ttt_short_conv_step(const e2ttt_conv_shape* s, const void* x, con
 size_t e2ttt_ssm_workspace_bytes(const e2ttt_ssm_shape* s, int for_bwd) {
   SsmDims d;
   if (ssm_dims("e2ttt_ssm_workspace_bytes", s, &d) != E2TTT_OK) return 0;
-  return for_bwd ? ssm_bwd_workspace_bytes(d) : ssm_fwd_bytes(d);
+  return for_bwd ? ssm_bwd_workspace_bytes(d) : ssm_fwd_layout(d).total;
 }
 
 size_t e2ttt_ssm_saved_bytes(const e2ttt_ssm_shape* s) {
@@ -274,7 +284,8 @@ e2ttt_status e2ttt_ssm_scan_fwd(const e2ttt_ssm_shape* s, const void* q, const v
     if (!q || !k || !v || !dt || !A || !y || !S_end)
       return failf(E2TTT_ERR_INVALID_ARG, "%s: q, k, v, dt, A, y and S_end must not be NULL", who);
     const SsmBytes n = ssm_bytes(d);
-    const size_t need = ssm_fwd_bytes(d);
+    const SsmFwdWs lay = ssm_fwd_layout(d);
+    const size_t need = lay.total;
     TRY(check_ws(who, ws, ws_bytes, need));
     TRY(check_aligned(who, n.es, {{q, 0, "q"}, {k, 0, "k"}, {v, 0, "v"}, {y, 0, "y"}}));
     TRY(check_aligned(who, 4, {{dt, 0, "dt"}, {A, 0, "A"}, {D, 0, "D"}, {S0, 0, "S0"},
@@ -283,9 +294,10 @@ e2ttt_status e2ttt_ssm_scan_fwd(const e2ttt_ssm_shape* s, const void* q, const v
                           {D, n.head, "D"}, {S0, n.S, "S0"}, {lengths, n.len, "lengths"}},
                     {{y, n.v, "y"}, {S_end, n.S, "S_end"}, {saved, n.saved, "saved_states"},
                      {ws, need, "workspace"}}));
-    float* states = saved ? saved : (float*)((char*)ws + up256((size_t)d.NC * d.B * d.H * 4));
-    SsmFwdArgs a{d, q, k, v, dt, A, D, S0, lengths, y, S_end, states, (float*)ws, (cudaStream_t)stream};
-    return check_run(ssm_fwd(a), who);
+    char* w = (char*)ws;
+    SsmFwdArgs a{d, q, k, v, dt, A, D, S0, lengths, y, S_end, saved ? saved : (float*)(w + lay.states),
+                 (float*)(w + lay.decay), (float*)(w + lay.logs), (int*)w, (cudaStream_t)stream};
+    return check_run(d.tc ? ssm_tc_fwd(a) : ssm_fwd(a), who);
   })
 }
 

@@ -40,8 +40,10 @@ struct SsmDims {
   int Q, NC;     // tokens per chunk, chunks
   int NPT;       // tiles of kSsmPT state rows
   bool bf16_act;
+  bool tc;       // chunks run on the tensor cores
 };
 constexpr int kSsmPT = 64;
+constexpr int kSsmTcChunk = 128;  // tokens per chunk on the tensor cores
 
 struct SsmFwdArgs {
   SsmDims s;
@@ -52,9 +54,17 @@ struct SsmFwdArgs {
   float* S_end;
   float* states;  // [NC][B*H][P][N]: saved_states or workspace
   float* decay;   // [NC][B*H] workspace
+  float* logs;    // tensor cores: the chunks' logarithms, workspace
+  int* status;    // device status word of the bounded waits
   cudaStream_t st;
 };
-cudaError_t ssm_fwd(const SsmFwdArgs& a);
+cudaError_t ssm_fwd(const SsmFwdArgs& a);     // CUDA cores, any shape
+cudaError_t ssm_tc_fwd(const SsmFwdArgs& a);  // tensor cores, shapes with tc set
+size_t ssm_tc_logs_bytes(const SsmDims& s);
+// The states' passage along the chunks (back: their adjoint's, from the end),
+// from `first` (NULL: zero); what is left after the last chunk goes to `last`.
+cudaError_t ssm_carry(const SsmDims& s, bool back, const float* first, const float* decay,
+                      float* states, float* last, cudaStream_t st);
 
 struct SsmBwdArgs {
   SsmDims s;
@@ -69,8 +79,20 @@ struct SsmBwdArgs {
   void* ws;
   cudaStream_t st;
 };
+// The backward's workspace, cut up.
+struct SsmBwdScratch {
+  int* status;
+  float *ends, *decay, *logs;  // [NC][B*H][P][N], [NC][B*H], the chunks' logarithms (tensor cores)
+  float *dq, *dk;              // [B*G][parts][T][N] sums over part of a group's heads
+  float* ddt;                  // [NPT][B*H][T]; the output itself where NPT is 1
+  float *dA, *dD;              // [NC][NPT][B*H]
+};
 size_t ssm_bwd_workspace_bytes(const SsmDims& s);
 cudaError_t ssm_bwd(const SsmBwdArgs& a);
+cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w);
+int ssm_tc_grad_parts(const SsmDims& s);
+// dq, dk (where there are several parts), ddt, dA and dD from their parts.
+cudaError_t ssm_grad_sums(const SsmBwdArgs& a, const SsmBwdScratch& w, int parts);
 
 struct SsmStepArgs {
   SsmDims s;

@@ -4,6 +4,8 @@
 // A chunk's work is a handful of small matrix products, done here from shared
 // memory by 16 x 16 threads with 4 x 4 results each; chunks meet only in their
 // states, which one elementwise pass carries along the tokens.
+#include <type_traits>
+
 #include "ssm.cuh"
 #include "trace.h"
 
@@ -94,9 +96,10 @@ __global__ void __launch_bounds__(kT)
     chunk_state_kernel(SsmDims s, const T* __restrict__ x, const T* __restrict__ y,
                        const float* __restrict__ dt, const float* __restrict__ A,
                        const int* __restrict__ lengths, float* __restrict__ states,
-                       float* __restrict__ decay) {
+                       float* __restrict__ decay, int* __restrict__ status) {
   extern __shared__ float sm[];
   const Where w = where(s, lengths);
+  if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0) *status = 0;  // nothing here waits
   const int Q = s.Q, N = s.N, XP = kSsmPT + 1, NP = N + 1;
   const ChunkLogs L = chunk_logs(sm, Q);
   float* xs = sm + 3 * Q;
@@ -130,19 +133,26 @@ __global__ void __launch_bounds__(kT)
 
 // Turns the chunks' own contributions into the states at their starts (REV 0,
 // from `first`) or the gradients at their ends (REV 1, from the last chunk
-// back); `last` gets what is left after the last one.
-template <int REV>
+// back); `last` gets what is left after the last one. Elementwise along the
+// chunks, bound by the states' bytes; V is float4 where rows and pointers allow.
+__device__ __forceinline__ void decay_add(float& run, float d, float own) { run = fmaf(d, run, own); }
+__device__ __forceinline__ void decay_add(float4& run, float d, const float4& own) {
+  run = float4{fmaf(d, run.x, own.x), fmaf(d, run.y, own.y), fmaf(d, run.z, own.z), fmaf(d, run.w, own.w)};
+}
+template <typename V, int REV>
 __global__ void __launch_bounds__(kT)
-    carry_kernel(int NC, int BH, long long PN, const float* __restrict__ first,
-                 const float* __restrict__ decay, float* __restrict__ states,
-                 float* __restrict__ last) {
+    carry_kernel(int NC, int BH, long long PN, const V* __restrict__ first,
+                 const float* __restrict__ decay, V* __restrict__ states, V* __restrict__ last) {
   const int bh = blockIdx.y;
   const long long i = (long long)blockIdx.x * kT + threadIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();
   if (i >= PN) return;
-  float run = first ? first[bh * PN + i] : 0.f;
+  V run = first ? first[bh * PN + i] : V{};
   constexpr int U = 8;
   for (int c0 = 0; c0 < NC; c0 += U) {
-    float own[U], d[U];
+    V own[U];
+    float d[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
@@ -156,7 +166,7 @@ __global__ void __launch_bounds__(kT)
       const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
       if (c0 + u < NC) {
         states[((long long)c * BH + bh) * PN + i] = run;
-        run = fmaf(d[u], run, own[u]);
+        decay_add(run, d[u], own[u]);
       }
     }
   }
@@ -531,46 +541,48 @@ cudaError_t allow_smem(F* f, size_t bytes) {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-struct BwdWs {
-  size_t ends, decay, dqp, dkp, ddtp, dAp, dDp, total;
-};
-BwdWs bwd_layout(const SsmDims& s) {
-  BwdWs L{};
+// Cuts up the backward's workspace (or, of a null one, only measures it).
+size_t cut_bwd(const SsmDims& s, char* ws, float* ddt, SsmBwdScratch* w) {
   size_t o = 0;
   const size_t f = sizeof(float), BH = (size_t)s.B * s.H;
-  auto take = [&](size_t n) { const size_t r = o; o = up256(o + n); return r; };
-  L.ends = take(s.NC * BH * s.P * s.N * f);
-  L.decay = take(s.NC * BH * f);
-  L.dqp = take(BH * s.NPT * s.T * s.N * f);
-  L.dkp = take(BH * s.NPT * s.T * s.N * f);
-  L.ddtp = take(s.NPT > 1 ? s.NPT * BH * s.T * f : 0);
-  L.dAp = take((size_t)s.NC * s.NPT * BH * f);
-  L.dDp = take((size_t)s.NC * s.NPT * BH * f);
-  L.total = o;
-  return L;
+  auto take = [&](size_t n) {
+    char* p = ws + o;
+    o = up256(o + n);
+    return (float*)p;
+  };
+  // One part per head and state tile on CUDA cores; none where the tensor cores'
+  // only part is the result.
+  const size_t parts = s.tc ? ssm_tc_grad_parts(s) : (size_t)s.H / s.G * s.NPT;
+  const size_t sums = s.tc && parts == 1 ? 0 : parts * s.B * s.G * s.T * s.N * f;
+  w->status = (int*)take(256);
+  w->ends = take(s.NC * BH * s.P * s.N * f);
+  w->decay = take(s.NC * BH * f);
+  w->logs = take(s.tc ? ssm_tc_logs_bytes(s) : 0);
+  w->dq = take(sums);
+  w->dk = take(sums);
+  w->ddt = s.NPT > 1 ? take(s.NPT * BH * s.T * f) : ddt;
+  w->dA = take((size_t)s.NC * s.NPT * BH * f);
+  w->dD = take((size_t)s.NC * s.NPT * BH * f);
+  return o;
 }
 
 template <typename T>
 cudaError_t fwd_t(const SsmFwdArgs& a) {
   const SsmDims& s = a.s;
   const dim3 grid(s.NC, s.B * s.H, s.NPT);
-  const long long PN = (long long)s.P * s.N;
   cudaError_t e;
   {
     E2TTT_TRACE("ssm_chunk_state", a.st);
     if ((e = allow_smem(chunk_state_kernel<T, 0>, state_smem(s))) != cudaSuccess) return e;
     chunk_state_kernel<T, 0><<<grid, kT, state_smem(s), a.st>>>(
-        s, (const T*)a.v, (const T*)a.k, a.dt, a.A, a.lengths, a.states, a.decay);
+        s, (const T*)a.v, (const T*)a.k, a.dt, a.A, a.lengths, a.states, a.decay, a.status);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  {
-    E2TTT_TRACE("ssm_carry", a.st);
-    carry_kernel<0><<<dim3((unsigned)((PN + kT - 1) / kT), s.B * s.H), kT, 0, a.st>>>(
-        s.NC, s.B * s.H, PN, a.S0, a.decay, a.states, a.S_end);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
+  if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, a.st)) != cudaSuccess) return e;
   E2TTT_TRACE("ssm_chunk_out", a.st);
-  auto kern = s.Q == 64 ? chunk_out_kernel<T, 4> : chunk_out_kernel<T, 2>;
+  auto kern = chunk_out_kernel<T, 2>;
+  if constexpr (std::is_same<T, float>::value)  // bf16 with so few columns runs on the tensor cores
+    if (s.Q == 64) kern = chunk_out_kernel<T, 4>;
   if ((e = allow_smem(kern, out_smem(s))) != cudaSuccess) return e;
   kern<<<grid, kT, out_smem(s), a.st>>>(s, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.dt, a.A,
                                         a.D, a.lengths, a.states, (T*)a.y);
@@ -578,64 +590,85 @@ cudaError_t fwd_t(const SsmFwdArgs& a) {
 }
 
 template <typename T>
-cudaError_t bwd_t(const SsmBwdArgs& a) {
+cudaError_t bwd_t(const SsmBwdArgs& a, const SsmBwdScratch& w) {
   const SsmDims& s = a.s;
-  const BwdWs L = bwd_layout(s);
-  char* w = (char*)a.ws;
-  float *ends = (float*)(w + L.ends), *decay = (float*)(w + L.decay), *dqp = (float*)(w + L.dqp),
-        *dkp = (float*)(w + L.dkp), *dAp = (float*)(w + L.dAp), *dDp = (float*)(w + L.dDp);
-  float* ddtp = s.NPT > 1 ? (float*)(w + L.ddtp) : a.ddt;
-  const int BH = s.B * s.H;
-  const dim3 grid(s.NC, BH, s.NPT);
-  const long long PN = (long long)s.P * s.N;
+  const dim3 grid(s.NC, s.B * s.H, s.NPT);
   cudaError_t e;
   {
     E2TTT_TRACE("ssm_chunk_dstate", a.st);
     if ((e = allow_smem(chunk_state_kernel<T, 1>, state_smem(s))) != cudaSuccess) return e;
     chunk_state_kernel<T, 1><<<grid, kT, state_smem(s), a.st>>>(
-        s, (const T*)a.dy, (const T*)a.q, a.dt, a.A, a.lengths, ends, decay);
+        s, (const T*)a.dy, (const T*)a.q, a.dt, a.A, a.lengths, w.ends, w.decay, w.status);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  {
-    E2TTT_TRACE("ssm_carry_back", a.st);
-    carry_kernel<1><<<dim3((unsigned)((PN + kT - 1) / kT), BH), kT, 0, a.st>>>(
-        s.NC, BH, PN, a.dS_end, decay, ends, a.dS0);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
+  if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, a.st)) != cudaSuccess) return e;
   {
     E2TTT_TRACE("ssm_chunk_grad", a.st);
-    auto kern = s.Q == 64 ? chunk_grad_kernel<T, 4> : chunk_grad_kernel<T, 2>;
+    auto kern = chunk_grad_kernel<T, 2>;
+    if constexpr (std::is_same<T, float>::value)  // bf16 with so few columns runs on the tensor cores
+      if (s.Q == 64) kern = chunk_grad_kernel<T, 4>;
     if ((e = allow_smem(kern, grad_smem(s))) != cudaSuccess) return e;
     kern<<<grid, kT, grad_smem(s), a.st>>>(s, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.dt, a.A,
-                                           a.D, a.lengths, a.states, ends, (const T*)a.dy, dqp, dkp,
-                                           (T*)a.dv, ddtp, dAp, dDp);
+                                           a.D, a.lengths, a.states, w.ends, (const T*)a.dy, w.dq, w.dk,
+                                           (T*)a.dv, w.ddt, w.dA, w.dD);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const long long row = (long long)s.T * s.N;
-  const dim3 gsum((unsigned)((row + kT - 1) / kT), s.B * s.G);
-  {
-    E2TTT_TRACE("ssm_group_sum", a.st);
-    group_sum_kernel<T><<<gsum, kT, 0, a.st>>>(dqp, s.H / s.G * s.NPT, row, (T*)a.dq);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    group_sum_kernel<T><<<gsum, kT, 0, a.st>>>(dkp, s.H / s.G * s.NPT, row, (T*)a.dk);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  if (s.NPT > 1) {
-    const long long n = (long long)BH * s.T;
-    E2TTT_TRACE("ssm_tile_sum", a.st);
-    tile_sum_kernel<<<(unsigned)((n + kT - 1) / kT), kT, 0, a.st>>>(ddtp, s.NPT, n, a.ddt);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  E2TTT_TRACE("ssm_head_sum", a.st);
-  head_sum_kernel<<<s.H, kT, 0, a.st>>>(dAp, dDp, s.NC * s.NPT * s.B, s.H, a.dA, a.dD);
-  return cudaGetLastError();
+  return ssm_grad_sums(a, w, s.H / s.G * s.NPT);
 }
 
 }  // namespace
 
-size_t ssm_bwd_workspace_bytes(const SsmDims& s) { return bwd_layout(s).total; }
+cudaError_t ssm_carry(const SsmDims& s, bool back, const float* first, const float* decay,
+                      float* states, float* last, cudaStream_t st) {
+  const int BH = s.B * s.H;
+  const long long PN = (long long)s.P * s.N;
+  E2TTT_TRACE(back ? "ssm_carry_back" : "ssm_carry", st);
+  if (PN % 4 == 0 && !(((uintptr_t)first | (uintptr_t)states | (uintptr_t)last) & 15)) {
+    const dim3 grid((unsigned)((PN / 4 + kT - 1) / kT), BH);
+    return launch_pdl(back ? carry_kernel<float4, 1> : carry_kernel<float4, 0>, grid, dim3(kT), 0, st, s.NC, BH,
+                      PN / 4, (const float4*)first, decay, (float4*)states, (float4*)last);
+  }
+  const dim3 grid((unsigned)((PN + kT - 1) / kT), BH);
+  return launch_pdl(back ? carry_kernel<float, 1> : carry_kernel<float, 0>, grid, dim3(kT), 0, st, s.NC, BH, PN,
+                    first, decay, states, last);
+}
+
+cudaError_t ssm_grad_sums(const SsmBwdArgs& a, const SsmBwdScratch& w, int parts) {
+  const SsmDims& s = a.s;
+  cudaError_t e;
+  const long long row = (long long)s.T * s.N, n = (long long)s.B * s.H * s.T;
+  const dim3 grid((unsigned)((row + kT - 1) / kT), s.B * s.G);
+  if (!s.tc || parts > 1) {
+    E2TTT_TRACE("ssm_group_sum", a.st);
+    for (int i = 0; i < 2; ++i) {
+      if (s.bf16_act)
+        group_sum_kernel<bf16><<<grid, kT, 0, a.st>>>(i ? w.dk : w.dq, parts, row, (bf16*)(i ? a.dk : a.dq));
+      else
+        group_sum_kernel<float><<<grid, kT, 0, a.st>>>(i ? w.dk : w.dq, parts, row, (float*)(i ? a.dk : a.dq));
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+  }
+  if (s.NPT > 1) {
+    E2TTT_TRACE("ssm_tile_sum", a.st);
+    tile_sum_kernel<<<(unsigned)((n + kT - 1) / kT), kT, 0, a.st>>>(w.ddt, s.NPT, n, a.ddt);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  E2TTT_TRACE("ssm_head_sum", a.st);
+  head_sum_kernel<<<s.H, kT, 0, a.st>>>(w.dA, w.dD, s.NC * s.NPT * s.B, s.H, a.dA, a.dD);
+  return cudaGetLastError();
+}
+
+size_t ssm_bwd_workspace_bytes(const SsmDims& s) {
+  SsmBwdScratch w;
+  return cut_bwd(s, nullptr, nullptr, &w);
+}
 cudaError_t ssm_fwd(const SsmFwdArgs& a) { return a.s.bf16_act ? fwd_t<bf16>(a) : fwd_t<float>(a); }
-cudaError_t ssm_bwd(const SsmBwdArgs& a) { return a.s.bf16_act ? bwd_t<bf16>(a) : bwd_t<float>(a); }
+cudaError_t ssm_bwd(const SsmBwdArgs& a) {
+  SsmBwdScratch w;
+  cut_bwd(a.s, (char*)a.ws, a.ddt, &w);
+  if (a.s.tc) return ssm_tc_bwd(a, w);
+  return a.s.bf16_act ? bwd_t<bf16>(a, w) : bwd_t<float>(a, w);
+}
 
 cudaError_t ssm_step(const SsmStepArgs& a) {
   const SsmDims& s = a.s;

@@ -1,0 +1,903 @@
+// State-space scan on the tensor cores (bf16 activations, at most 128 state
+// columns; any alignment, odd sizes padded with zeros in shared memory). The
+// mathematics is in ssm.cuh; chunks are of 128 tokens, so that every product of
+// a chunk is one 128-row tcgen05 tile with its accumulator in tensor memory.
+//
+// A matrix lies in shared memory as columns of 64 bf16 (128-byte rows, 128-byte
+// swizzle). The same bytes serve as a K-major operand (its columns contracted)
+// and as an MN-major one (its rows contracted), so nothing is transposed.
+//
+// Precision. Inputs are bf16 and enter the products as they are. What is not an
+// input is rounded once to bf16 where its product ends in a bf16 result (the
+// decayed scores, the state in y and dv); where the product ends in an fp32
+// result (the states, and the dots behind ddt and dA) it enters as three bf16
+// terms that together hold all 24 bits of it, each with a product of its own.
+#include <initializer_list>
+
+#include "ssm.cuh"
+#include "tc_gemm2.cuh"
+#include "trace.h"
+
+namespace e2ttt {
+namespace {
+
+using tc2::idesc;
+using tc2::smem_u32;
+
+constexpr int kQ = kSsmTcChunk;  // tokens per chunk
+constexpr int kThreads = 256;    // 8 warps: tensor-memory lanes 32 (w & 3), column half w >> 2
+constexpr int kPT = kSsmPT;
+
+// Byte offset of 16-byte piece `j` (8 columns) of row r in a tile of ROWS rows.
+template <int ROWS>
+__device__ __forceinline__ uint32_t piece(int r, int j) {
+  return (uint32_t)((j >> 3) * ROWS * 128 + r * 128 + (((j & 7) ^ (r & 7)) << 4));
+}
+
+// Descriptor of such a tile: `mn` for the MN-major reading (64-column blocks
+// ROWS * 128 bytes apart).
+template <int ROWS>
+__device__ __forceinline__ uint64_t tile_desc(const uint8_t* p, bool mn) {
+  uint64_t d = (uint64_t)((smem_u32(p) & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(mn ? (ROWS * 128) >> 4 : 1) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// Start-address advance of contraction step k (16 deep), in 16-byte units.
+template <int ROWS, bool MN>
+__device__ __forceinline__ uint32_t step_off(int k) {
+  return MN ? (uint32_t)(k * 2048) >> 4 : (uint32_t)((k >> 2) * ROWS * 128 + (k & 3) * 32) >> 4;
+}
+// acc[128][N] (+)= A B over `steps` steps of 16; A of AROWS stored rows, B of BROWS.
+template <int AROWS, bool AMN, int BROWS, bool BMN, int N>
+__device__ __forceinline__ void mma(uint32_t acc, const uint8_t* a, const uint8_t* b, int steps,
+                                    bool add) {
+  const uint64_t da = tile_desc<AROWS>(a, AMN), db = tile_desc<BROWS>(b, BMN);
+  constexpr uint32_t id = idesc(128, N, AMN, BMN);
+  for (int k = 0; k < steps; ++k)
+    tc::mma_bf16(acc, da + step_off<AROWS, AMN>(k), db + step_off<BROWS, BMN>(k), id, add || k);
+}
+
+// The waits of one block on its MMAs: one mbarrier, one phase per commit.
+struct Mmas {
+  uint64_t* bar;
+  uint32_t phase;
+  int* status;
+  // True (for the whole block) once the last commit has completed; false, with
+  // the status word set, after about a second without it.
+  __device__ __forceinline__ bool wait() {
+    const bool ok = tc::mbar_wait(bar, phase);
+    if (!ok && threadIdx.x == 0) atomicExch(status, tc2::kErrMma);
+    const bool all = __syncthreads_and(ok);
+    // on giving up: once more, so that the MMAs do not outlive their memory
+    if (!all) (void)tc::mbar_wait(bar, phase);
+    phase ^= 1u;
+    tc::tc_fence_after();
+    return all;
+  }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Eight consecutive values of a row of `cols` from column c on, zeros beyond.
+__device__ __forceinline__ uint4 load8(const bf16* row, int c, int cols) {
+  uint4 r{0, 0, 0, 0};
+  bf16* p = reinterpret_cast<bf16*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < cols) p[i] = row[c + i];
+  return r;
+}
+
+// Rows [0, n) of src (pitch ld, `cols` columns) into a tile of kQ rows and
+// `blocks` 64-column blocks; everything else is zero. vec: 16-byte copies apply.
+__device__ __forceinline__ void load_rows(uint8_t* tile, int blocks, const bf16* src, long long ld, int n,
+                                          int cols, bool vec) {
+  const uint32_t base = smem_u32(tile);
+  const int per = blocks * 8;
+  for (int i = threadIdx.x; i < kQ * per; i += kThreads) {
+    const int r = i / per, j = i - r * per;
+    const bool on = r < n && j * 8 < cols;
+    const uint32_t at = piece<kQ>(r, j);
+    if (vec)
+      cp16(base + at, on ? src + (long long)r * ld + j * 8 : src, on);
+    else
+      *reinterpret_cast<uint4*>(tile + at) =
+          on ? load8(src + (long long)r * ld, j * 8, cols) : uint4{0, 0, 0, 0};
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// Eight values to a row of which `left` columns remain.
+__device__ __forceinline__ void store8(bf16* out, const uint4& w, int left, bool vec) {
+  if (vec && left >= 8) {
+    *reinterpret_cast<uint4*>(out) = w;
+  } else {
+    const bf16* e = reinterpret_cast<const bf16*>(&w);
+    for (int j = 0; j < 8 && j < left; ++j) out[j] = e[j];
+  }
+}
+
+// f as three bf16 terms: f = t0 + t1 + t2 to 24 bits.
+__device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
+  uint32_t* o[3] = {&t[0].x, &t[1].x, &t[2].x};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = f[2 * i], b = f[2 * i + 1];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const uint32_t p = pack2(a, b);
+      o[j][i] = p;
+      a -= lo_f(p);
+      b -= hi_f(p);
+    }
+  }
+}
+
+// Per chunk in global memory, written once per call by logs_kernel: [3][kQ] hi,
+// lo and eta of its tokens (see ChunkLogs).
+struct __align__(16) Logs {
+  float hi[kQ], lo[kQ], eta[kQ];
+};
+
+__device__ __forceinline__ ChunkLogs logs_view(float* p) {
+  ChunkLogs L;
+  L.hi = p;
+  L.lo = p + kQ;
+  L.eta = p + 2 * kQ;
+  L.Q1 = kQ - 1;
+  return L;
+}
+
+// One warp per (batch row, head, chunk): its logs and decay e^{c_Q}; resets the
+// status word of the launches that follow.
+__global__ void __launch_bounds__(128)
+    logs_kernel(SsmDims s, const float* __restrict__ dt, const float* __restrict__ A,
+                const int* __restrict__ lengths, float* __restrict__ logs,
+                float* __restrict__ decay, int* __restrict__ status) {
+  __shared__ Logs sm[4];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x * 4 + w, bh = blockIdx.y, b = bh / s.H;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x == 0 && bh == 0 && threadIdx.x == 0) *status = 0;
+  if (c >= s.NC) return;
+  const ChunkLogs L = logs_view(sm[w].hi);
+  const int t0 = c * kQ;
+  fill_chunk_logs(L, dt + (long long)bh * s.T + t0, A[bh - b * s.H],
+                  min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ));
+  __syncwarp();
+  float4* out = reinterpret_cast<float4*>(logs + ((long long)bh * s.NC + c) * 3 * kQ);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) out[i * 32 + lane] = reinterpret_cast<const float4*>(sm[w].hi)[i * 32 + lane];
+  if (lane == 0) decay[(long long)c * s.B * s.H + bh] = L.from_start(kQ - 1);
+}
+
+__device__ __forceinline__ void load_logs(const ChunkLogs& L, const float* logs, int bh, int NC, int c) {
+  const float4* p = reinterpret_cast<const float4*>(logs + ((long long)bh * NC + c) * 3 * kQ);
+  if (threadIdx.x < 3 * kQ / 4) reinterpret_cast<float4*>(L.hi)[threadIdx.x] = p[threadIdx.x];
+}
+
+// Set-up and tear-down that every kernel shares: an mbarrier and `COLS` columns
+// of tensor memory.
+template <int COLS>
+__device__ __forceinline__ uint32_t block_begin(uint64_t* bar, uint32_t* slot) {
+  if (threadIdx.x == 0) {
+    tc::mbar_init(bar, 1);
+    tc::fence_mbar_init();
+  }
+  if (threadIdx.x < 32) {
+    tc::tmem_alloc(slot, COLS);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  return *slot;
+}
+template <int COLS>
+__device__ __forceinline__ void block_end(uint32_t tmem) {
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (threadIdx.x < 32) tc::tmem_dealloc(tmem, COLS);
+}
+// Shared-memory writes of this thread become visible to the MMAs; then the block meets.
+__device__ __forceinline__ void publish() {
+  tc::fence_async_smem();
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+}
+
+__device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+// ------------------------------------------------------------------ chunk states
+// states[c][bh][p][n] = sum_s w_s x_s[p] y_s[n]: with REV 0 x = v, y = k,
+// w_s = e^{c_Q-c_s} eta_s; with REV 1 x = dy, y = q, w_t = e^{c_t}. D[n][p] on
+// the tensor cores (128 state columns as rows of the tile): y contracted over
+// its rows, w x in three terms.
+template <int REV>
+__global__ void __launch_bounds__(kThreads, 2)
+    state_kernel(SsmDims s, const bf16* __restrict__ x, const bf16* __restrict__ y,
+                 const float* __restrict__ logs, const int* __restrict__ lengths,
+                 float* __restrict__ states, int* __restrict__ status, bool vec) {
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(16) float slog[3 * kQ];
+  __shared__ uint64_t bar;
+  __shared__ uint32_t slot;
+  uint8_t* ys = align1k(raw);   // [kQ][128]
+  uint8_t* xs = ys + kQ * 256;  // three of [kQ][64]
+  const int bh = blockIdx.y, b = bh / s.H, h = bh - b * s.H, g = h / (s.H / s.G);
+  const int c = blockIdx.x, t0 = c * kQ, p0 = blockIdx.z * kPT, np = min(kPT, s.P - p0);
+  const ChunkLogs L = logs_view(slog);
+  const uint32_t tmem = block_begin<64>(&bar, &slot);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n = min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ);
+  load_rows(ys, 2, y + (((long long)b * s.G + g) * s.T + t0) * s.N, s.N, n, s.N, vec);
+  load_logs(L, logs, bh, s.NC, c);
+  const int r = threadIdx.x >> 1, j0 = (threadIdx.x & 1) * 4;
+  const bf16* xr = x + ((long long)bh * s.T + t0 + r) * s.P + p0;
+  uint4 xv[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int col = (j0 + j) * 8;
+    xv[j] = uint4{0, 0, 0, 0};
+    if (r < n && col < np) xv[j] = vec ? *reinterpret_cast<const uint4*>(xr + col) : load8(xr, col, np);
+  }
+  __syncthreads();
+  const float w = REV ? L.from_start(r) : L.to_end(r) * L.eta[r];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t* u = &xv[j].x;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = w * lo_f(u[i]);
+      f[2 * i + 1] = w * hi_f(u[i]);
+    }
+    uint4 t[3];
+    split3(f, t);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      *reinterpret_cast<uint4*>(xs + i * kQ * 128 + piece<kQ>(r, j0 + j)) = t[i];
+  }
+  cp_wait();
+  publish();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) mma<kQ, true, kQ, true, 64>(tmem, ys, xs + i * kQ * 128, kQ / 16, i > 0);
+    tc::mma_commit(&bar);
+  }
+  Mmas done{&bar, 0u, status};
+  if (done.wait()) {
+    const int warp = threadIdx.x >> 5, quad = warp & 3, half = warp >> 2;
+    const int nn = quad * 32 + (threadIdx.x & 31);
+    float v[32];
+    tc::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + half * 32, v);
+    float* out = states + (((long long)c * s.B * s.H + bh) * s.P + p0 + half * 32) * s.N + nn;
+    if (nn < s.N)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (half * 32 + j < np) out[(long long)j * s.N] = v[j];
+  }
+  block_end<64>(tmem);
+}
+
+// ------------------------------------------------------------------ outputs
+// The decay between token t (this thread's row) and the columns of a 32-token
+// block: exactly within the row's own block, and as e^{c_t - c_r} e^{c_r - c_s}
+// with r the last token of an earlier block (two factors that are both at most
+// one for a decaying state), so that only a quarter of them takes an exponential
+// each. `tail[s]` holds e^{c_r - c_s}.
+__device__ __forceinline__ void fill_tails(const ChunkLogs& L, float* tail) {
+  if (threadIdx.x < kQ) tail[threadIdx.x] = L.decay(threadIdx.x | 31, threadIdx.x);
+}
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 2)
+    out_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,
+               const bf16* __restrict__ v, const float* __restrict__ logs,
+               const float* __restrict__ D, const int* __restrict__ lengths,
+               const float* __restrict__ states, bf16* __restrict__ y, int* __restrict__ status,
+               bool vec) {
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(16) float slog[3 * kQ];
+  __shared__ float tail[kQ];
+  __shared__ uint64_t bar;
+  __shared__ uint32_t slot;
+  uint8_t* qs = align1k(raw);          // [kQ][NB * 64]
+  uint8_t* vs = qs + NB * kQ * 128;    // [kQ][64]
+  uint8_t* Ss = vs + kQ * 128;         // [64][NB * 64]
+  uint8_t* ks = Ss + NB * kPT * 128;   // [kQ][NB * 64], then the scores [kQ][kQ]
+  const int bh = blockIdx.y, b = bh / s.H, h = bh - b * s.H, g = h / (s.H / s.G);
+  const int c = blockIdx.x, t0 = c * kQ, p0 = blockIdx.z * kPT, np = min(kPT, s.P - p0);
+  const ChunkLogs L = logs_view(slog);
+  const uint32_t tmem = block_begin<256>(&bar, &slot);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n = min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ);
+  const long long qo = (((long long)b * s.G + g) * s.T + t0) * s.N;
+  load_rows(qs, NB, q + qo, s.N, n, s.N, vec);
+  load_rows(ks, NB, k + qo, s.N, n, s.N, vec);
+  load_rows(vs, 1, v + ((long long)bh * s.T + t0) * s.P + p0, s.P, n, np, vec);
+  load_logs(L, logs, bh, s.NC, c);
+  const float* S = states + (((long long)c * s.B * s.H + bh) * s.P + p0) * s.N;
+  for (int i = threadIdx.x; i < kPT * NB * 8; i += kThreads) {
+    const int p = i / (NB * 8), j = i - p * (NB * 8);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = p < np && j * 8 + e < s.N ? S[(long long)p * s.N + j * 8 + e] : 0.f;
+    *reinterpret_cast<uint4*>(Ss + piece<kPT>(p, j)) =
+        uint4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+  }
+  cp_wait();
+  publish();
+  const int nsteps = (s.N + 15) / 16;
+  constexpr uint32_t kM = 0, kYi = 128, kYd = 192;
+  Mmas done{&bar, 0u, status};
+  if (threadIdx.x == 0) {
+    mma<kQ, false, kQ, false, 128>(tmem + kM, qs, ks, nsteps, false);
+    mma<kQ, false, kPT, false, 64>(tmem + kYi, qs, Ss, nsteps, false);
+    tc::mma_commit(&bar);
+  }
+  fill_tails(L, tail);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = warp >> 2;
+  const int t = quad * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  if (done.wait()) {
+#pragma unroll 1
+    for (int cb = half; cb < 4; cb += 2) {
+      uint4 o[4];
+      uint32_t* ow = &o[0].x;
+      if (cb <= quad) {
+        float m[32];
+        tc::tmem_ld32(lanes + kM + cb * 32, m);
+        const float row = cb < quad ? L.decay(t, cb * 32 + 31) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int u = cb * 32 + i;
+          if (cb < quad)
+            m[i] *= row * tail[u] * L.eta[u];
+          else
+            m[i] = u <= t ? m[i] * (L.decay(t, u) * L.eta[u]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ow[i] = pack2(m[2 * i], m[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = uint4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(ks + piece<kQ>(t, cb * 4 + i)) = o[i];
+    }
+    publish();
+    if (threadIdx.x == 0) {
+      mma<kQ, false, kQ, true, 64>(tmem + kYd, ks, vs, kQ / 16, false);
+      tc::mma_commit(&bar);
+    }
+    if (done.wait()) {
+      float yi[32], yd[32];
+      tc::tmem_ld32(lanes + kYi + half * 32, yi);
+      tc::tmem_ld32(lanes + kYd + half * 32, yd);
+      const float f = L.from_start(t), Dh = D ? D[h] : 0.f;
+      bf16* out = y + ((long long)bh * s.T + t0 + t) * s.P + p0 + half * 32;
+      if (t0 + t < s.T)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 xv = *reinterpret_cast<const uint4*>(vs + piece<kQ>(t, half * 4 + i));
+          const uint32_t* xu = &xv.x;
+          uint4 o;
+          uint32_t* ou = &o.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int a = i * 8 + e * 2;
+            const float y0 = fmaf(f, yi[a], yd[a]) + Dh * lo_f(xu[e]);
+            const float y1 = fmaf(f, yi[a + 1], yd[a + 1]) + Dh * hi_f(xu[e]);
+            ou[e] = t < n ? pack2(y0, y1) : 0u;
+          }
+          store8(out + i * 8, o, np - (half * 32 + i * 8), vec);
+        }
+    }
+  }
+  block_end<256>(tmem);
+}
+
+// ------------------------------------------------------------------ gradients
+// 16 columns of one value per (row = lane, column): the sum over the warp's
+// lanes of column `lane & 15`, to that lane.
+__device__ __forceinline__ float column_sums(float (&v)[16], int lane) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float send = up ? v[i] : v[i + o];
+      const float keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(~0u, send, o);
+    }
+  return v[0] + __shfl_xor_sync(~0u, v[0], 16);
+}
+// 16 columns of this thread's lane from each of two places.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t a, uint32_t b, float (&x)[16], float (&y)[16]) {
+  uint32_t r[16], u[16];
+#define E2TTT_LD16(R, AT)                                                                            \
+  asm volatile(                                                                                      \
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"                                                       \
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"              \
+      : "=r"(R[0]), "=r"(R[1]), "=r"(R[2]), "=r"(R[3]), "=r"(R[4]), "=r"(R[5]), "=r"(R[6]),          \
+        "=r"(R[7]), "=r"(R[8]), "=r"(R[9]), "=r"(R[10]), "=r"(R[11]), "=r"(R[12]), "=r"(R[13]),      \
+        "=r"(R[14]), "=r"(R[15])                                                                     \
+      : "r"(AT)                                                                                      \
+      : "memory")
+  E2TTT_LD16(r, a);
+  E2TTT_LD16(u, b);
+#undef E2TTT_LD16
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    asm volatile("" : "+r"(r[i]), "+r"(u[i]));  // no use of them moves before the wait
+    x[i] = __uint_as_float(r[i]);
+    y[i] = __uint_as_float(u[i]);
+  }
+}
+
+struct GradOut {
+  float *dq, *dk;    // [B*G][parts][T][N]: sums over a part's heads, fp32
+  bf16 *dq16, *dk16; // the results themselves, where there is one part
+  bf16* dv;
+  float *ddt, *dA, *dD;
+};
+
+// All gradients of one chunk for a run of heads of one group (and their tiles of
+// 64 state rows: `items`). dq and dk add up over the items on chip: the products
+// with the decayed scores in tensor memory, the states' parts in registers (their
+// rows are scaled item by item).
+//   tensor memory: [0, 256) scratch (S^T dy | X^T v; then q k^T | dy v^T; then the
+//   two parts of dv), [256, 384) dq, [384, 512) dk
+//   shared memory: q, k; v, dy of the item; S and X in three terms, later
+//   overwritten by the two score matrices (X's first term stays)
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    grad_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,
+                const bf16* __restrict__ v, const bf16* __restrict__ dy,
+                const float* __restrict__ logs, const float* __restrict__ A,
+                const float* __restrict__ D, const int* __restrict__ lengths,
+                const float* __restrict__ states, const float* __restrict__ ends, GradOut o,
+                int per, int* __restrict__ status, bool vec) {
+  constexpr int kTerm = NB * kPT * 128;  // bytes of one term of a state
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(16) float slog[3 * kQ];
+  __shared__ float tail[kQ], rows[2][kQ], cols[4][kQ], rdr[2][kQ], src[2][kQ], diag[2][kQ], warp_ip[8];
+  __shared__ uint64_t bar;
+  __shared__ uint32_t slot;
+  uint8_t* qs = align1k(raw);
+  uint8_t* ks = qs + NB * kQ * 128;
+  uint8_t* vs = ks + NB * kQ * 128;
+  uint8_t* gs = vs + kQ * 128;
+  uint8_t* W1 = gs + kQ * 128;   // e^{c_t-c_s} q_t.k_s, [t][s]
+  uint8_t* W2 = W1 + kQ * 256;   // e^{c_t-c_s} eta_s dy_t.v_s
+  uint8_t* Xs = W2 + kQ * 256;   // X, first term
+  uint8_t* St = W1;              // S, three terms, and X's second and third, under W1 and W2
+  const int c = blockIdx.x, bg = blockIdx.y, b = bg / s.G, g = bg - b * s.G, split = blockIdx.z;
+  const int HG = s.H / s.G, items = HG * s.NPT, BH = s.B * s.H, t0 = c * kQ;
+  const ChunkLogs L = logs_view(slog);
+  const uint32_t tmem = block_begin<512>(&bar, &slot);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n = min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ);
+  const long long qo = ((long long)bg * s.T + t0) * s.N;
+  load_rows(qs, NB, q + qo, s.N, n, s.N, vec);
+  load_rows(ks, NB, k + qo, s.N, n, s.N, vec);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = warp >> 2;
+  const int t = quad * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  constexpr uint32_t kDq = 256, kDk = 384;
+  constexpr int HC = NB * 32;  // this thread's columns of dq and dk: [half * HC, half * HC + HC)
+  const int nsteps = (s.N + 15) / 16;
+  Mmas done{&bar, 0u, status};
+  float dqa[HC], dka[HC];
+#pragma unroll
+  for (int i = 0; i < HC; ++i) dqa[i] = dka[i] = 0.f;
+  bool ok = true;
+
+  const int i0 = split * per, i1 = min(items, i0 + per);
+#pragma unroll 1
+  for (int it = i0; it < i1 && ok; ++it) {
+    const int h = g * HG + it / s.NPT, pt = it % s.NPT, bh = b * s.H + h;
+    const int p0 = pt * kPT, np = min(kPT, s.P - p0);
+    const long long vo = ((long long)bh * s.T + t0) * s.P + p0;
+    load_rows(vs, 1, v + vo, s.P, n, np, vec);
+    load_rows(gs, 1, dy + vo, s.P, n, np, vec);
+    load_logs(L, logs, bh, s.NC, c);
+    // S and X, as three terms each, and <S, X>
+    {
+      const long long so = (((long long)c * BH + bh) * s.P + p0) * s.N;
+      float ip = 0.f;
+      for (int i = threadIdx.x; i < kPT * NB * 8; i += kThreads) {
+        const int p = i / (NB * 8), j = i - p * (NB * 8);
+        float f[8], x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool in = p < np && j * 8 + e < s.N;
+          const long long at = so + (long long)p * s.N + j * 8 + e;
+          f[e] = in ? states[at] : 0.f;
+          x[e] = in ? ends[at] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ip = fmaf(f[e], x[e], ip);
+        const uint32_t at = piece<kPT>(p, j);
+        uint4 term[3];
+        split3(f, term);
+#pragma unroll
+        for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4*>(St + m * kTerm + at) = term[m];
+        split3(x, term);
+        *reinterpret_cast<uint4*>(Xs + at) = term[0];
+        *reinterpret_cast<uint4*>(St + 3 * kTerm + at) = term[1];
+        if constexpr (NB == 1)
+          *reinterpret_cast<uint4*>(St + 4 * kTerm + at) = term[2];
+        else
+          *reinterpret_cast<uint4*>(Xs + kTerm + at) = term[2];
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) ip += __shfl_xor_sync(~0u, ip, d);
+      if (lane == 0) warp_ip[warp] = ip;
+    }
+    cp_wait();
+    publish();
+    if (threadIdx.x == 0) {
+      const uint8_t* x2 = NB == 1 ? St + 4 * kTerm : Xs + kTerm;
+      for (int m = 0; m < 3; ++m) mma<kQ, false, kPT, true, NB * 64>(tmem, gs, St + m * kTerm, kPT / 16, m > 0);
+      mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, Xs, kPT / 16, false);
+      mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, St + 3 * kTerm, kPT / 16, true);
+      mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, x2, kPT / 16, true);
+      tc::mma_commit(&bar);
+    }
+    fill_tails(L, tail);
+    if (!(ok = done.wait())) break;
+    // the states' parts of dq and dk, and their dots with q and k
+    {
+      const float f = L.from_start(t), e = L.to_end(t), eta = L.eta[t];
+      float rd = 0.f, sd = 0.f;
+#pragma unroll
+      for (int cb = 0; cb < NB; ++cb) {
+        float a[32];
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          tc::tmem_ld32(lanes + which * 128 + half * HC + cb * 32, a);
+          const uint8_t* tile = which ? ks : qs;
+          const float scale = which ? e : f;
+          float dot = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 r = *reinterpret_cast<const uint4*>(tile + piece<kQ>(t, (half * HC + cb * 32) / 8 + j));
+            const uint32_t* u = &r.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = j * 8 + i * 2;
+              dot = fmaf(a[at], lo_f(u[i]), dot);
+              dot = fmaf(a[at + 1], hi_f(u[i]), dot);
+            }
+          }
+          if (which) {
+            sd = fmaf(dot, scale, sd);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) dka[cb * 32 + i] = fmaf(a[i], scale * eta, dka[cb * 32 + i]);
+          } else {
+            rd = fmaf(dot, scale, rd);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) dqa[cb * 32 + i] = fmaf(a[i], scale, dqa[cb * 32 + i]);
+          }
+        }
+      }
+      rdr[half][t] = rd;
+      src[half][t] = sd;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (threadIdx.x == 0) {
+      mma<kQ, false, kQ, false, 128>(tmem, qs, ks, nsteps, false);
+      mma<kQ, false, kQ, false, 128>(tmem + 128, gs, vs, kPT / 16, false);
+      tc::mma_commit(&bar);
+    }
+    if (!(ok = done.wait())) break;
+    // the decayed scores, and the row and column sums of Z off its diagonal
+    float zrow = 0.f;
+#pragma unroll 1
+    for (int cb = half; cb < 4; cb += 2) {
+#pragma unroll 1
+      for (int sub = 0; sub < 2; ++sub) {
+        const int u0 = cb * 32 + sub * 16;
+        uint4 o1[2] = {}, o2[2] = {};
+        if (cb <= quad) {
+          float m[16], kk[16], off[16];
+          tmem_ld16x2(lanes + u0, lanes + 128 + u0, m, kk);
+          const float rowf = cb < quad ? L.decay(t, cb * 32 + 31) : 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int u = u0 + i;
+            const float e = cb < quad ? rowf * tail[u] : u <= t ? L.decay(t, u) : 0.f;
+            const float a = u <= t ? e * m[i] : 0.f, d = u <= t ? kk[i] : 0.f;
+            const float r = a * d;
+            if (u == t) {
+              diag[0][t] = r;
+              diag[1][t] = d;
+            }
+            off[i] = u < t ? r : 0.f;
+            zrow = fmaf(off[i], L.eta[u], zrow);
+            m[i] = a;
+            kk[i] = d * (e * L.eta[u]);
+          }
+          uint32_t *w1 = &o1[0].x, *w2 = &o2[0].x;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            w1[i] = pack2(m[2 * i], m[2 * i + 1]);
+            w2[i] = pack2(kk[2 * i], kk[2 * i + 1]);
+          }
+          const float sum = column_sums(off, lane);
+          if (lane < 16) cols[quad][u0 + lane] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          *reinterpret_cast<uint4*>(W1 + piece<kQ>(t, u0 / 8 + i)) = o1[i];
+          *reinterpret_cast<uint4*>(W2 + piece<kQ>(t, u0 / 8 + i)) = o2[i];
+        }
+      }
+    }
+    rows[half][t] = zrow;
+    publish();
+    if (threadIdx.x == 0) {
+      mma<kQ, true, kQ, true, 64>(tmem, W1, gs, kQ / 16, false);
+      mma<kQ, false, kPT, false, 64>(tmem + 64, ks, Xs, nsteps, false);
+      mma<kQ, false, kQ, true, NB * 64>(tmem + kDq, W2, ks, kQ / 16, it > i0);
+      mma<kQ, true, kQ, true, NB * 64>(tmem + kDk, W2, qs, kQ / 16, it > i0);
+      tc::mma_commit(&bar);
+    }
+    if (warp == 0) {
+      // ddt, dA, dD: lane l has the tokens 4 l .. 4 l + 3
+      double a4[4], b4[4], as = 0.0, bs = 0.0;
+      float off4[4], src4[4], dd = 0.f, ip = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ip += warp_ip[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = lane * 4 + i;
+        float off = 0.f;
+        for (int qd = r >> 5; qd < 4; ++qd) off += cols[qd][r];
+        off4[i] = off;
+        src4[i] = src[0][r] + src[1][r];
+        a4[i] = (double)(rows[0][r] + rows[1][r]) - (double)(L.eta[r] * off) + (double)(rdr[0][r] + rdr[1][r]);
+        b4[i] = (double)L.eta[r] * src4[i];
+        as += a4[i];
+        bs += b4[i];
+        dd += diag[1][r];
+      }
+      double after = as, before = bs;  // of this lane's tokens on; up to them
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double x = __shfl_down_sync(~0u, after, d), y = __shfl_up_sync(~0u, before, d);
+        if (lane + d < 32) after += x;
+        if (lane >= d) before += y;
+      }
+      before -= bs;
+      const double through = (double)L.from_start(kQ - 1) * ip;
+      const float Ah = A[h];
+      double dA = 0.0;
+      float* out = o.ddt + ((long long)pt * BH + bh) * s.T + t0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = lane * 4 + i;
+        const double dl = after + before + through;
+        after -= a4[i];
+        before += b4[i];
+        dA += L.eta[r] * dl;
+        if (t0 + r < s.T) out[r] = r < n ? (float)(Ah * dl + off4[i] + diag[0][r] + src4[i]) : 0.f;
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        dA += __shfl_xor_sync(~0u, dA, d);
+        dd += __shfl_xor_sync(~0u, dd, d);
+      }
+      if (lane == 0) {
+        const long long at = ((long long)c * s.NPT + pt) * BH + bh;
+        o.dA[at] = (float)dA;
+        o.dD[at] = dd;
+      }
+      __syncwarp();
+    }
+    if (!(ok = done.wait())) break;
+    {
+      float a1[32], a2[32];
+      tc::tmem_ld32(lanes + half * 32, a1);
+      tc::tmem_ld32(lanes + 64 + half * 32, a2);
+      const float e = L.to_end(t), eta = L.eta[t], Dh = D ? D[h] : 0.f;
+      bf16* out = o.dv + vo + (long long)t * s.P + half * 32;
+      if (t0 + t < s.T)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 r = *reinterpret_cast<const uint4*>(gs + piece<kQ>(t, half * 4 + i));
+          const uint32_t* u = &r.x;
+          uint4 w;
+          uint32_t* wu = &w.x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int x = i * 8 + j * 2;
+            const float d0 = fmaf(eta, fmaf(e, a2[x], a1[x]), Dh * lo_f(u[j]));
+            const float d1 = fmaf(eta, fmaf(e, a2[x + 1], a1[x + 1]), Dh * hi_f(u[j]));
+            wu[j] = t < n ? pack2(d0, d1) : 0u;
+          }
+          store8(out + i * 8, w, np - (half * 32 + i * 8), vec);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();  // the item's tiles, logs and sums are free for the next one
+    tc::tc_fence_after();
+  }
+  if (ok) {
+    const int parts = gridDim.z;
+    const bool there = t0 + t < s.T;
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+      for (int cb = 0; cb < NB; ++cb) {
+        float a[32];
+        tc::tmem_ld32(lanes + (which ? kDk : kDq) + half * HC + cb * 32, a);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a[i] = t < n ? a[i] + (which ? dka : dqa)[cb * 32 + i] : 0.f;
+        const int col = half * HC + cb * 32;
+        if (!there) continue;
+        if (parts == 1) {
+          bf16* out = (which ? o.dk16 : o.dq16) + qo + (long long)t * s.N + col;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            store8(out + i * 8,
+                   uint4{pack2(a[i * 8], a[i * 8 + 1]), pack2(a[i * 8 + 2], a[i * 8 + 3]),
+                         pack2(a[i * 8 + 4], a[i * 8 + 5]), pack2(a[i * 8 + 6], a[i * 8 + 7])},
+                   s.N - col - i * 8, vec);
+        } else {
+          float* out = (which ? o.dk : o.dq) + (((long long)bg * parts + split) * s.T + t0 + t) * s.N + col;
+          if (s.N % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (col + i * 4 < s.N)
+                *reinterpret_cast<float4*>(out + i * 4) = float4{a[i * 4], a[i * 4 + 1], a[i * 4 + 2], a[i * 4 + 3]};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col + i < s.N) out[i] = a[i];
+          }
+        }
+      }
+  }
+  block_end<512>(tmem);
+}
+
+size_t state_smem() { return 1024 + kQ * 256 + 3 * kQ * 128; }
+template <int NB>
+size_t out_smem() {
+  return 1024 + NB * kQ * 128 + kQ * 128 + NB * kPT * 128 + kQ * 256;
+}
+
+template <int NB>
+size_t grad_smem() {
+  return 1024 + 2 * NB * kQ * 128 + 2 * kQ * 128 + 2 * kQ * 256 + (NB == 1 ? 1 : 2) * NB * kPT * 128;
+}
+
+// How many blocks share the heads of a group (and their state tiles) in the
+// gradients. A block's fixed part (q, k, the results) weighs about a third of an
+// item; every part more is one more fp32 copy of dq and dk to write and add up.
+int grad_parts(const SsmDims& s) {
+  constexpr int kSms = 148;
+  const long long items = (long long)s.H / s.G * s.NPT, base = (long long)s.B * s.G * s.NC;
+  int best = 1;
+  double cost = 1e300;
+  for (long long ns = 1; ns <= items; ++ns) {
+    const long long per = (items + ns - 1) / ns;
+    if ((items + per - 1) / per != ns) continue;
+    const double c = (double)((base * ns + kSms - 1) / kSms) * (per + 0.35) + 0.04 * ns * base / kSms;
+    if (c < cost) cost = c, best = (int)ns;
+  }
+  return best;
+}
+
+template <class F>
+cudaError_t allow_smem(F* f, size_t bytes) {
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+bool vectors(const SsmDims& s, std::initializer_list<const void*> ps) {
+  if (s.N % 8 || s.P % 8) return false;
+  for (const void* p : ps)
+    if ((uintptr_t)p & 15) return false;
+  return true;
+}
+
+}  // namespace
+
+size_t ssm_tc_logs_bytes(const SsmDims& s) {
+  return (size_t)s.B * s.H * s.NC * 3 * kQ * sizeof(float);
+}
+
+int ssm_tc_grad_parts(const SsmDims& s) { return grad_parts(s); }
+
+cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
+  const SsmDims& s = a.s;
+  const int BH = s.B * s.H, parts = grad_parts(s);
+  const long long items = (long long)s.H / s.G * s.NPT;
+  const int per = (int)((items + parts - 1) / parts);
+  const bool vec = vectors(s, {a.q, a.k, a.v, a.dy, a.dq, a.dk, a.dv});
+  cudaError_t e;
+  {
+    E2TTT_TRACE("ssm_logs", a.st);
+    e = launch_pdl(logs_kernel, dim3((s.NC + 3) / 4, BH), dim3(128), 0, a.st, s, a.dt, a.A, a.lengths, w.logs,
+                   w.decay, w.status);
+    if (e != cudaSuccess) return e;
+  }
+  {
+    E2TTT_TRACE("ssm_chunk_dstate", a.st);
+    if ((e = allow_smem(state_kernel<1>, state_smem())) != cudaSuccess) return e;
+    e = launch_pdl(state_kernel<1>, dim3(s.NC, BH, s.NPT), dim3(kThreads), state_smem(), a.st, s,
+                   (const bf16*)a.dy, (const bf16*)a.q, (const float*)w.logs, a.lengths, w.ends, w.status, vec);
+    if (e != cudaSuccess) return e;
+  }
+  if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, a.st)) != cudaSuccess) return e;
+  {
+    E2TTT_TRACE("ssm_chunk_grad", a.st);
+    auto kern = s.N <= 64 ? grad_kernel<1> : grad_kernel<2>;
+    const size_t smem = s.N <= 64 ? grad_smem<1>() : grad_smem<2>();
+    if ((e = allow_smem(kern, smem)) != cudaSuccess) return e;
+    const GradOut o{w.dq, w.dk, (bf16*)a.dq, (bf16*)a.dk, (bf16*)a.dv, w.ddt, w.dA, w.dD};
+    e = launch_pdl(kern, dim3(s.NC, s.B * s.G, parts), dim3(kThreads), smem, a.st, s, (const bf16*)a.q,
+                   (const bf16*)a.k, (const bf16*)a.v, (const bf16*)a.dy, (const float*)w.logs, a.A, a.D, a.lengths,
+                   a.states, (const float*)w.ends, o, per, w.status, vec);
+    if (e != cudaSuccess) return e;
+  }
+  return ssm_grad_sums(a, w, parts);
+}
+
+cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
+  const SsmDims& s = a.s;
+  const int BH = s.B * s.H;
+  const dim3 grid(s.NC, BH, s.NPT);
+  const bool vec = vectors(s, {a.q, a.k, a.v, a.y});
+  cudaError_t e;
+  {
+    E2TTT_TRACE("ssm_logs", a.st);
+    e = launch_pdl(logs_kernel, dim3((s.NC + 3) / 4, BH), dim3(128), 0, a.st, s, a.dt, a.A, a.lengths, a.logs,
+                   a.decay, a.status);
+    if (e != cudaSuccess) return e;
+  }
+  {
+    E2TTT_TRACE("ssm_chunk_state", a.st);
+    if ((e = allow_smem(state_kernel<0>, state_smem())) != cudaSuccess) return e;
+    e = launch_pdl(state_kernel<0>, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.v,
+                   (const bf16*)a.k, (const float*)a.logs, a.lengths, a.states, a.status, vec);
+    if (e != cudaSuccess) return e;
+  }
+  if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, a.st)) != cudaSuccess) return e;
+  E2TTT_TRACE("ssm_chunk_out", a.st);
+  auto kern = s.N <= 64 ? out_kernel<1> : out_kernel<2>;
+  const size_t smem = s.N <= 64 ? out_smem<1>() : out_smem<2>();
+  if ((e = allow_smem(kern, smem)) != cudaSuccess) return e;
+  return launch_pdl(kern, grid, dim3(kThreads), smem, a.st, s, (const bf16*)a.q, (const bf16*)a.k,
+                    (const bf16*)a.v, (const float*)a.logs, a.D, a.lengths, (const float*)a.states,
+                    (bf16*)a.y, a.status, vec);
+}
+
+}  // namespace e2ttt

@@ -65,9 +65,9 @@ inline e2ttt_status check_aligned(const char* who, size_t align, std::initialize
   return E2TTT_OK;
 }
 
-inline bool all_aligned16(std::initializer_list<const void*> ps) {
+inline bool all_aligned(size_t align, std::initializer_list<const void*> ps) {
   for (const void* p : ps)
-    if (((uintptr_t)p) & 15) return false;
+    if (((uintptr_t)p) & (align - 1)) return false;
   return true;
 }
 

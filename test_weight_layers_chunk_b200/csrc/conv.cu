@@ -8,7 +8,7 @@
 //   dx_t = sum_j w_j dz_{t+(W-1)-j},  dw_j = sum_t dz_t x_{t-(W-1)+j},  dbias = sum_t dz_t.
 //
 // Bound by HBM: the forward reads x and writes y once, the backward reads x and
-// dy and writes dx. A thread owns one 16-byte vector of channels and walks a run
+// dy and writes dx. A thread owns four consecutive channels and walks a run
 // of R consecutive tokens with the last W inputs (and, backward, the last W dz)
 // in registers, so a run re-reads only the W-1 tokens before it (and the
 // backward the W-1 after it), which the neighbouring run has just brought into
@@ -22,51 +22,126 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxW = 8;
 
-// 1 / (1 + exp(-z)); exp overflows to infinity for z << 0, whose reciprocal is 0.
-__device__ __forceinline__ float sigmoid_fast(float z) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+// Pairs of fp32 values, for the packed fp32 instructions: one issue for two
+// channels, each rounded as by itself.
+typedef float2 F2;
+__device__ __forceinline__ unsigned long long bits(F2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ F2 pair(unsigned long long b) {
+  F2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return pair(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return pair(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return pair(r);
+}
+__device__ __forceinline__ F2 both(float x) { return F2{x, x}; }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
+// 1 / (1 + exp(-z)); exp overflows to infinity for z << 0, whose reciprocal is 0.
+__device__ __forceinline__ F2 sigmoid2(F2 z) {
+  const F2 a = mul2(z, both(-1.4426950408889634f));
+  const F2 b = add2(F2{ex2(a.x), ex2(a.y)}, both(1.0f));
+  return F2{rcp(b.x), rcp(b.y)};
+}
+
 template <typename T, int VEC> struct VecOf;
-template <> struct VecOf<bf16, 8> { typedef uint4 type; };
+template <> struct VecOf<bf16, 4> { typedef uint2 type; };
 template <> struct VecOf<float, 4> { typedef uint4 type; };
 template <> struct VecOf<bf16, 1> { typedef unsigned short type; };
 template <> struct VecOf<float, 1> { typedef unsigned int type; };
 
+// A thread's VEC channels as NP pairs (one channel: a pair with a spare half).
 template <typename T, int VEC>
-__device__ __forceinline__ void unpack(const typename VecOf<T, VEC>::type& r, float (&f)[VEC]) {
+__device__ __forceinline__ void unpack(const typename VecOf<T, VEC>::type& r, F2 (&f)[(VEC + 1) / 2]) {
   const T* p = reinterpret_cast<const T*>(&r);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) f[i] = to_f<T>(p[i]);
+  for (int i = 0; i < (VEC + 1) / 2; ++i) f[i] = F2{to_f<T>(p[2 * i]), VEC > 1 ? to_f<T>(p[VEC > 1 ? 2 * i + 1 : 0]) : 0.f};
 }
 template <typename T, int VEC>
-__device__ __forceinline__ typename VecOf<T, VEC>::type pack(const float (&f)[VEC]) {
+__device__ __forceinline__ typename VecOf<T, VEC>::type pack(const F2 (&f)[(VEC + 1) / 2]) {
   typename VecOf<T, VEC>::type r;
   T* p = reinterpret_cast<T*>(&r);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) p[i] = from_f<T>(f[i]);
+  for (int i = 0; i < (VEC + 1) / 2; ++i) {
+    p[2 * i] = from_f<T>(f[i].x);
+    if (VEC > 1) p[VEC > 1 ? 2 * i + 1 : 0] = from_f<T>(f[i].y);
+  }
   return r;
+}
+template <int NP>
+__device__ __forceinline__ void zero(F2 (&f)[NP]) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) f[i] = both(0.f);
 }
 
 struct Geo {
   int H, T, d, nvec, nvt, rows;  // vectors per token, vectors per block, runs per block
   int runs;                      // runs of R tokens in T
   int R;
-  bool silu;
 };
 
 __device__ __forceinline__ int row_length(const int* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
+// The W taps of VEC consecutive channels: contiguous in memory, read as 16-byte
+// vectors where the first one is aligned.
+template <int W, int VEC>
+__device__ __forceinline__ void load_taps(const float* w, F2 (&wr)[W][(VEC + 1) / 2]) {
+  float flat[W * VEC];
+  if (VEC > 1 && (((uintptr_t)w) & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i < W * VEC / 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(w + 4 * i);
+      flat[4 * i] = v.x, flat[4 * i + 1] = v.y, flat[4 * i + 2] = v.z, flat[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W * VEC; ++i) flat[i] = w[i];
+  }
+#pragma unroll
+  for (int i = 0; i < (VEC + 1) / 2; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      wr[j][i] = F2{flat[2 * i * W + j], VEC > 1 ? flat[(VEC > 1 ? 2 * i + 1 : 0) * W + j] : 0.f};
+}
+template <int VEC>
+__device__ __forceinline__ void load_bias(const float* bias, F2 (&br)[(VEC + 1) / 2]) {
+#pragma unroll
+  for (int i = 0; i < (VEC + 1) / 2; ++i)
+    br[i] = bias ? F2{bias[2 * i], VEC > 1 ? bias[VEC > 1 ? 2 * i + 1 : 0] : 0.f} : both(0.f);
+}
+
 // Input at position i of the sequence [state; x[0..len)] (i = 0 is the oldest
 // history row), zero outside it.
 template <typename T, int VEC>
 __device__ __forceinline__ void load_seq(const T* xrow, const T* srow, int i, int W1, int len,
-                                         int d, int c0, float (&f)[VEC]) {
+                                         int d, int c0, F2 (&f)[(VEC + 1) / 2]) {
   typedef typename VecOf<T, VEC>::type V;
   const T* p = nullptr;
   if (i >= W1) {
@@ -74,16 +149,26 @@ __device__ __forceinline__ void load_seq(const T* xrow, const T* srow, int i, in
   } else if (srow && i >= 0) {
     p = srow + (long long)i * d + c0;
   }
-  if (p) {
+  if (p)
     unpack<T, VEC>(*reinterpret_cast<const V*>(p), f);
-  } else {
+  else
+    zero(f);
+}
+
+// N raw rows of a token matrix from p on.
+template <typename V, typename T, int N>
+__device__ __forceinline__ void load_batch(V (&raw)[N], const T* p, int d) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = 0.f;
+  for (int i = 0; i < N; ++i) {
+    raw[i] = *reinterpret_cast<const V*>(p);
+    p += d;
   }
 }
 
-template <typename T, int W, int VEC>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(Geo g, const T* __restrict__ x,
+constexpr int kBatch = 4;  // tokens whose loads are in flight together
+
+template <typename T, int W, int VEC, bool SILU>
+__global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 2) conv_fwd_kernel(Geo g, const T* __restrict__ x,
                                                             const float* __restrict__ w,
                                                             const float* __restrict__ bias,
                                                             const T* __restrict__ state,
@@ -91,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(Geo g, const T* __re
                                                             T* __restrict__ y,
                                                             T* __restrict__ state_end) {
   typedef typename VecOf<T, VEC>::type V;
-  constexpr int W1 = W - 1;
+  constexpr int W1 = W - 1, NP = (VEC + 1) / 2;
   const int bh = blockIdx.y, h = bh % g.H;
   const int vi = blockIdx.z * g.nvt + threadIdx.x % g.nvt;
   const int run = blockIdx.x * g.rows + threadIdx.x / g.nvt;
@@ -100,52 +185,62 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(Geo g, const T* __re
   const T* xrow = x + (long long)bh * g.T * g.d;
   T* yrow = y + (long long)bh * g.T * g.d;
   const T* srow = state ? state + (long long)bh * W1 * g.d : nullptr;
+  const int t0 = run * g.R, t1 = min(t0 + g.R, g.T), end = min(t1, len);
+  const int full = end > t0 ? (end - t0) / kBatch : 0;  // whole batches of tokens that exist
 
-  float wr[W][VEC], br[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    br[e] = bias ? bias[h * g.d + c0 + e] : 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) wr[j][e] = w[((long long)h * g.d + c0 + e) * W + j];
-  }
-  const int t0 = run * g.R, t1 = min(t0 + g.R, g.T);
-  float win[W][VEC];  // the W inputs that end at the current token
+  const T* xp = xrow + (long long)t0 * g.d + c0;
+  T* yp = yrow + (long long)t0 * g.d + c0;
+  V next[kBatch];
+  if (full) load_batch(next, xp, g.d);
+  F2 wr[W][NP], br[NP];
+  load_taps<W, VEC>(w + ((long long)h * g.d + c0) * W, wr);
+  load_bias<VEC>(bias ? bias + h * g.d + c0 : nullptr, br);
+  F2 win[W][NP];  // the W inputs that end at the current token
 #pragma unroll
   for (int j = 0; j < W1; ++j) load_seq<T, VEC>(xrow, srow, t0 + j, W1, len, g.d, c0, win[j]);
 
-  constexpr int BATCH = 8;
-  for (int tb = t0; tb < t1; tb += BATCH) {
-    V raw[BATCH];
+  auto token = [&](const V& raw, F2(&o)[NP]) {
+    unpack<T, VEC>(raw, win[W1]);
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      raw[i] = V{};
-      if (tb + i < t1 && tb + i < len)
-        raw[i] = *reinterpret_cast<const V*>(xrow + (long long)(tb + i) * g.d + c0);
+    for (int e = 0; e < NP; ++e) {
+      F2 z = br[e];
+#pragma unroll
+      for (int j = 0; j < W; ++j) z = fma2(wr[j][e], win[j][e], z);
+      o[e] = SILU ? mul2(z, sigmoid2(z)) : z;
+#pragma unroll
+      for (int j = 0; j < W1; ++j) win[j][e] = win[j + 1][e];
     }
+  };
+#pragma unroll 1
+  for (int n = 0; n < full; ++n) {
+    V raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int t = tb + i;
-      unpack<T, VEC>(raw[i], win[W1]);
-      float o[VEC];
+    for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
+    xp += (long long)kBatch * g.d;
+    if (n + 1 < full) load_batch(next, xp, g.d);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        float z = br[e];
-#pragma unroll
-        for (int j = 0; j < W; ++j) z = fmaf(wr[j][e], win[j][e], z);
-        z = g.silu ? z * sigmoid_fast(z) : z;
-        o[e] = t < len ? z : 0.f;
-      }
-      if (t < t1) *reinterpret_cast<V*>(yrow + (long long)t * g.d + c0) = pack<T, VEC>(o);
-#pragma unroll
-      for (int j = 0; j < W1; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+    for (int i = 0; i < kBatch; ++i) {
+      F2 o[NP];
+      token(raw[i], o);
+      *reinterpret_cast<V*>(yp) = pack<T, VEC>(o);
+      yp += g.d;
     }
+  }
+#pragma unroll 1
+  for (int t = t0 + full * kBatch; t < t1; ++t) {
+    F2 o[NP];
+    V raw{};
+    if (t < end) raw = *reinterpret_cast<const V*>(xp);
+    token(raw, o);
+    if (t >= end) zero(o);
+    *reinterpret_cast<V*>(yp) = pack<T, VEC>(o);
+    xp += g.d;
+    yp += g.d;
   }
   if (state_end && run == 0) {
 #pragma unroll
     for (int j = 0; j < W1; ++j) {
-      float f[VEC];
+      F2 f[NP];
       load_seq<T, VEC>(xrow, srow, len + j, W1, len, g.d, c0, f);
       *reinterpret_cast<V*>(state_end + ((long long)bh * W1 + j) * g.d + c0) = pack<T, VEC>(f);
     }
@@ -153,15 +248,16 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(Geo g, const T* __re
 }
 
 // part [B * gridDim.x][H][W + 1][d]: this block's sums of dz x (taps 0..W-1) and dz.
-template <typename T, int W, int VEC>
-__global__ void __launch_bounds__(kThreads)
+// A run's walk goes W - 1 tokens past its end: their dz reach back into it.
+template <typename T, int W, int VEC, bool SILU>
+__global__ void __launch_bounds__(kThreads, W <= 4 ? 2 : 1)
     conv_bwd_kernel(Geo g, const T* __restrict__ x, const float* __restrict__ w,
                     const float* __restrict__ bias, const T* __restrict__ state,
                     const int* __restrict__ lengths, const T* __restrict__ dy,
                     const T* __restrict__ dstate_end, T* __restrict__ dx, T* __restrict__ dstate,
                     float* __restrict__ part) {
   typedef typename VecOf<T, VEC>::type V;
-  constexpr int W1 = W - 1;
+  constexpr int W1 = W - 1, NP = (VEC + 1) / 2;
   extern __shared__ float sums[];  // [blockDim.x][VEC]
   const int bh = blockIdx.y, h = bh % g.H, b = bh / g.H;
   const int vl = threadIdx.x % g.nvt, vi = blockIdx.z * g.nvt + vl, c0 = vi * VEC;
@@ -172,92 +268,125 @@ __global__ void __launch_bounds__(kThreads)
   T* dxrow = dx + (long long)bh * g.T * g.d;
   const T* srow = state ? state + (long long)bh * W1 * g.d : nullptr;
 
-  float wr[W][VEC], br[VEC], dw[W][VEC], db[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    br[e] = on && bias ? bias[h * g.d + c0 + e] : 0.f;
-    db[e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      wr[j][e] = on ? w[((long long)h * g.d + c0 + e) * W + j] : 0.f;
-      dw[j][e] = 0.f;
-    }
+  F2 wr[W][NP], br[NP], dw[W][NP], db[NP];
+  if (on) {
+    load_taps<W, VEC>(w + ((long long)h * g.d + c0) * W, wr);
+    load_bias<VEC>(bias ? bias + h * g.d + c0 : nullptr, br);
   }
+  zero(db);
+#pragma unroll
+  for (int j = 0; j < W; ++j) zero(dw[j]);
+#pragma unroll 1
   for (int run = blockIdx.x * g.rows + threadIdx.x / g.nvt; on && run < g.runs;
        run += gridDim.x * g.rows) {
-    const int t0 = run * g.R, t1 = min(t0 + g.R, g.T);
-    float win[W][VEC], dz[W][VEC];  // dz[j]: of the token j before the current one
+    const int t0 = run * g.R, t1 = min(t0 + g.R, g.T), last = t1 + W1;
+    const int end = min(t1, len), full = end > t0 ? (end - t0) / kBatch : 0;
+    const T* xp = xrow + (long long)t0 * g.d + c0;
+    const T* gp = dyrow + (long long)t0 * g.d + c0;
+    V nx[kBatch], nd[kBatch];
+    if (full) {
+      load_batch(nx, xp, g.d);
+      load_batch(nd, gp, g.d);
+    }
+    F2 win[W][NP], dz[W][NP];  // dz[j]: of the token j before the current one
 #pragma unroll
-    for (int j = 0; j < W; ++j)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) dz[j][e] = 0.f;
+    for (int j = 0; j < W; ++j) zero(dz[j]);
 #pragma unroll
     for (int j = 0; j < W1; ++j) load_seq<T, VEC>(xrow, srow, t0 + j, W1, len, g.d, c0, win[j]);
-    constexpr int BATCH = 4;
-    for (int tb = t0; tb < t1 + W1; tb += BATCH) {
-      V rx[BATCH], rd[BATCH];
+
+    // One token s: its dz, its sums (`mine`: it belongs to this run), and the
+    // gradient o of sequence position s (x of token s - W1, or history row s).
+    auto token = [&](const V& rx, const V& rd, bool mine, F2(&o)[NP]) {
+      F2 gy[NP];
+      unpack<T, VEC>(rx, win[W1]);
+      unpack<T, VEC>(rd, gy);
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        rx[i] = V{};
-        rd[i] = V{};
-        if (tb + i < t1 + W1 && tb + i < len) {
-          rx[i] = *reinterpret_cast<const V*>(xrow + (long long)(tb + i) * g.d + c0);
-          rd[i] = *reinterpret_cast<const V*>(dyrow + (long long)(tb + i) * g.d + c0);
+      for (int e = 0; e < NP; ++e) {
+        if constexpr (SILU) {
+          F2 z = br[e];
+#pragma unroll
+          for (int j = 0; j < W; ++j) z = fma2(wr[j][e], win[j][e], z);
+          const F2 sg = sigmoid2(z);
+          const F2 f = fma2(z, fma2(sg, both(-1.f), both(1.f)), both(1.f));  // y' = sg (1 + z (1 - sg))
+          dz[0][e] = mul2(gy[e], mul2(sg, f));
+        } else {
+          dz[0][e] = gy[e];
         }
+        if (mine) {
+          db[e] = add2(db[e], dz[0][e]);
+#pragma unroll
+          for (int j = 0; j < W; ++j) dw[j][e] = fma2(dz[0][e], win[j][e], dw[j][e]);
+        }
+        o[e] = mul2(wr[0][e], dz[0][e]);
+#pragma unroll
+        for (int j = 1; j < W; ++j) o[e] = fma2(wr[j][e], dz[j][e], o[e]);
+#pragma unroll
+        for (int j = 0; j < W1; ++j) win[j][e] = win[j + 1][e];
+#pragma unroll
+        for (int j = W1; j > 0; --j) dz[j][e] = dz[j - 1][e];
+      }
+    };
+    T* op = dxrow + (long long)(t0 - W1) * g.d + c0;  // where token s's o goes
+#pragma unroll 1
+    for (int n = 0; n < full; ++n) {
+      V rx[kBatch], rd[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) rx[i] = nx[i], rd[i] = nd[i];
+      xp += (long long)kBatch * g.d;
+      gp += (long long)kBatch * g.d;
+      if (n + 1 < full) {
+        load_batch(nx, xp, g.d);
+        load_batch(nd, gp, g.d);
       }
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const int s = tb + i;
-        float gy[VEC], o[VEC];
-        unpack<T, VEC>(rx[i], win[W1]);
-        unpack<T, VEC>(rd[i], gy);
-        const bool mine = s < t1;  // its sums belong to this run
+      for (int i = 0; i < kBatch; ++i) {
+        F2 o[NP];
+        token(rx[i], rd[i], true, o);
+        if (n * kBatch + i >= W1)
+          *reinterpret_cast<V*>(op) = pack<T, VEC>(o);
+        else if (run == 0 && dstate)
+          *reinterpret_cast<V*>(dstate + ((long long)bh * W1 + n * kBatch + i) * g.d + c0) = pack<T, VEC>(o);
+        op += g.d;
+      }
+    }
+    int s = t0 + full * kBatch;
+    if (s == t1 && last <= len && full * kBatch >= W1) {
+      // the tokens past the run, all there
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float z = br[e];
-#pragma unroll
-          for (int j = 0; j < W; ++j) z = fmaf(wr[j][e], win[j][e], z);
-          float f = 1.f;
-          if (g.silu) {
-            const float sg = sigmoid_fast(z);
-            f = sg * fmaf(z, 1.f - sg, 1.f);
-          }
-          dz[0][e] = s < len ? gy[e] * f : 0.f;
-          const float own = mine ? dz[0][e] : 0.f;
-          db[e] += own;
-#pragma unroll
-          for (int j = 0; j < W; ++j) dw[j][e] = fmaf(own, win[j][e], dw[j][e]);
-          o[e] = 0.f;
-#pragma unroll
-          for (int j = 0; j < W; ++j) o[e] = fmaf(wr[j][e], dz[j][e], o[e]);
-        }
-        // o is the gradient of sequence position s (x of token s - W1, or history row s)
+      for (int i = 0; i < W1; ++i) {
+        F2 o[NP];
+        token(*reinterpret_cast<const V*>(xp), *reinterpret_cast<const V*>(gp), false, o);
+        *reinterpret_cast<V*>(op) = pack<T, VEC>(o);
+        xp += g.d;
+        gp += g.d;
+        op += g.d;
+      }
+    } else {
+#pragma unroll 1
+      for (; s < last; ++s) {
         const int t = s - W1;
-        if (s < t1 + W1 && (t >= t0 || (t < 0 && run == 0))) {
-          const int je = s - len;  // which row of state_end this input is, if any
-          if (dstate_end && je >= 0 && je < W1) {
-            float f[VEC];
-            unpack<T, VEC>(*reinterpret_cast<const V*>(
-                               dstate_end + ((long long)bh * W1 + je) * g.d + c0), f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] += f[e];
-          }
-          if (t >= len) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = 0.f;
-          }
-          if (t >= 0)
-            *reinterpret_cast<V*>(dxrow + (long long)t * g.d + c0) = pack<T, VEC>(o);
-          else if (dstate)
-            *reinterpret_cast<V*>(dstate + ((long long)bh * W1 + s) * g.d + c0) = pack<T, VEC>(o);
+        F2 o[NP];
+        V vx{}, vd{};
+        if (s < len) {
+          vx = *reinterpret_cast<const V*>(xp);
+          vd = *reinterpret_cast<const V*>(gp);
         }
+        token(vx, vd, s < t1, o);
+        const int je = s - len;  // which row of state_end this input is, if any
+        if (dstate_end && je >= 0 && je < W1) {
+          F2 f[NP];
+          unpack<T, VEC>(*reinterpret_cast<const V*>(dstate_end + ((long long)bh * W1 + je) * g.d + c0), f);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-          for (int j = 0; j < W1; ++j) win[j][e] = win[j + 1][e];
-#pragma unroll
-          for (int j = W1; j > 0; --j) dz[j][e] = dz[j - 1][e];
+          for (int e = 0; e < NP; ++e) o[e] = add2(o[e], f[e]);
         }
+        if (t >= len) zero(o);
+        if (t >= t0)
+          *reinterpret_cast<V*>(op) = pack<T, VEC>(o);
+        else if (run == 0 && dstate)
+          *reinterpret_cast<V*>(dstate + ((long long)bh * W1 + s) * g.d + c0) = pack<T, VEC>(o);
+        xp += g.d;
+        gp += g.d;
+        op += g.d;
       }
     }
   }
@@ -267,7 +396,11 @@ __global__ void __launch_bounds__(kThreads)
   for (int j = 0; j <= W; ++j) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) sums[threadIdx.x * VEC + e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+    for (int e = 0; e < NP; ++e) {
+      const F2 v = j < W ? dw[j < W ? j : 0][e] : db[e];
+      sums[threadIdx.x * VEC + 2 * e] = v.x;
+      if (VEC > 1) sums[threadIdx.x * VEC + 2 * e + 1] = v.y;
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < g.nvt * VEC; i += blockDim.x) {
       const int c = blockIdx.z * g.nvt * VEC + i;
@@ -309,7 +442,7 @@ __global__ void __launch_bounds__(kThreads)
                      const float* __restrict__ w, const float* __restrict__ bias,
                      T* __restrict__ state, T* __restrict__ y) {
   typedef typename VecOf<T, VEC>::type V;
-  constexpr int W1 = W - 1;
+  constexpr int W1 = W - 1, NP = (VEC + 1) / 2;
   const int nvec = d / VEC;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (id >= (long long)BH * nvec) return;
@@ -319,18 +452,18 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int j = 0; j < W1; ++j) raw[j] = *reinterpret_cast<const V*>(srow + (long long)j * d);
   raw[W1] = *reinterpret_cast<const V*>(x + (long long)bh * d + c0);
-  float o[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = bias ? bias[h * d + c0 + e] : 0.f;
+  F2 wr[W][NP], o[NP];
+  load_taps<W, VEC>(w + ((long long)h * d + c0) * W, wr);
+  load_bias<VEC>(bias ? bias + h * d + c0 : nullptr, o);
 #pragma unroll
   for (int j = 0; j < W; ++j) {
-    float f[VEC];
+    F2 f[NP];
     unpack<T, VEC>(raw[j], f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) o[e] = fmaf(w[((long long)h * d + c0 + e) * W + j], f[e], o[e]);
+    for (int e = 0; e < NP; ++e) o[e] = fma2(wr[j][e], f[e], o[e]);
   }
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = silu ? o[e] * sigmoid_fast(o[e]) : o[e];
+  for (int e = 0; e < NP; ++e) o[e] = silu ? mul2(o[e], sigmoid2(o[e])) : o[e];
   *reinterpret_cast<V*>(y + (long long)bh * d + c0) = pack<T, VEC>(o);
 #pragma unroll
   for (int j = 0; j < W1; ++j) *reinterpret_cast<V*>(srow + (long long)j * d) = raw[j + 1];
@@ -341,11 +474,13 @@ Geo geometry(const ConvDims& s, int vec) {
   g.H = s.H;
   g.T = s.T;
   g.d = s.d;
-  g.silu = s.silu;
   g.nvec = s.d / vec;
   g.nvt = g.nvec < kThreads ? g.nvec : kThreads;
   g.rows = kThreads / g.nvt;
-  g.R = 16;
+  // Long runs re-read and recompute less (W - 1 tokens a run); short ones give
+  // more threads. The longest that still gives every SM 768 threads.
+  g.R = 32;
+  while (g.R > 8 && (long long)s.B * s.H * g.nvec * ((s.T + g.R - 1) / g.R) < 148LL * 768) g.R /= 2;
   g.runs = (s.T + g.R - 1) / g.R;
   return g;
 }
@@ -364,7 +499,8 @@ cudaError_t fwd_t(const ConvArgs& a, void* y, void* state_end) {
   const Geo g = geometry(a.s, VEC);
   dim3 grid((g.runs + g.rows - 1) / g.rows, a.s.B * a.s.H, (g.nvec + g.nvt - 1) / g.nvt);
   E2TTT_TRACE("conv_fwd", a.st);
-  conv_fwd_kernel<T, W, VEC><<<grid, g.nvt * g.rows, 0, a.st>>>(
+  auto kern = a.s.silu ? conv_fwd_kernel<T, W, VEC, true> : conv_fwd_kernel<T, W, VEC, false>;
+  kern<<<grid, g.nvt * g.rows, 0, a.st>>>(
       g, (const T*)a.x, a.w, a.bias, (const T*)a.state, a.lengths, (T*)y, (T*)state_end);
   return cudaGetLastError();
 }
@@ -378,7 +514,8 @@ cudaError_t bwd_t(const ConvArgs& a, const void* dy, const void* dstate_end, voi
   const int threads = g.nvt * g.rows;
   {
     E2TTT_TRACE("conv_bwd", a.st);
-    conv_bwd_kernel<T, W, VEC><<<grid, threads, threads * VEC * sizeof(float), a.st>>>(
+    auto kern = a.s.silu ? conv_bwd_kernel<T, W, VEC, true> : conv_bwd_kernel<T, W, VEC, false>;
+    kern<<<grid, threads, threads * VEC * sizeof(float), a.st>>>(
         g, (const T*)a.x, a.w, a.bias, (const T*)a.state, a.lengths, (const T*)dy,
         (const T*)dstate_end, (T*)dx, (T*)dstate, (float*)ws);
     cudaError_t e = cudaGetLastError();
@@ -414,7 +551,7 @@ cudaError_t step_t(const ConvArgs& a, void* state, void* y) {
   return cudaErrorInvalidValue;
 #define CONV_DISPATCH(F, ...)                          \
   if (a.s.bf16_act) {                                  \
-    if (a.vec) { CONV_WIDTHS(F, bf16, 8, __VA_ARGS__) } \
+    if (a.vec) { CONV_WIDTHS(F, bf16, 4, __VA_ARGS__) } \
     CONV_WIDTHS(F, bf16, 1, __VA_ARGS__)               \
   }                                                    \
   if (a.vec) { CONV_WIDTHS(F, float, 4, __VA_ARGS__) } \
@@ -425,7 +562,7 @@ cudaError_t step_t(const ConvArgs& a, void* state, void* y) {
 size_t conv_bwd_workspace_bytes(const ConvDims& s) {
   // whichever of the vector and single-channel forms runs (alignment decides at the call)
   size_t most = 0;
-  for (int vec : {1, s.bf16_act ? 8 : 4}) {
+  for (int vec : {1, 4}) {
     if (s.d % vec) continue;
     const size_t n = (size_t)s.B * bwd_blocks_x(s, geometry(s, vec)) * s.H * (s.W + 1) * s.d * sizeof(float);
     if (n > most) most = n;

@@ -5,12 +5,14 @@
 // Bound by HBM: the norm reads every gradient once; the clip reads them again
 // and writes them, and reads nothing where the norm is within max_norm and the
 // clip is in place. The tensors are cut into pieces of kPiece elements; block i
-// takes the pieces i, i + grid, ... of the whole list, so one launch serves
+// takes an equal range of the pieces of the whole list, so one launch serves
 // many small tensors as well as a few large ones (the list travels as a kernel
 // parameter, kMany tensors to a launch). Squares are summed in fp32 over one
 // 16-byte vector, then in fp64, to one partial per block; the clip's blocks each
 // add up all partials themselves, in the same order, so no block waits for
-// another and results repeat bit for bit.
+// another and results repeat bit for bit. A block of either pass has the same
+// range of pieces and the clip walks it backwards, so that what the norm read
+// last is still in L2.
 #include "seq_ops.h"
 #include "trace.h"
 
@@ -18,7 +20,7 @@ namespace e2ttt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 8192;
+constexpr int kPiece = 16384;
 constexpr int kFew = 32, kMany = 480;
 
 struct Item {
@@ -46,22 +48,24 @@ __device__ __forceinline__ int find(const List<MAX>& l, unsigned p) {
   return lo;
 }
 
+// First piece of block b's range.
+__device__ __forceinline__ unsigned range_start(unsigned pieces, unsigned b) {
+  return (unsigned)((unsigned long long)pieces * b / gridDim.x);
+}
+
 template <typename T> struct Wide { static constexpr int N = 16 / sizeof(T); };
 
-// Sum of squares of one vector. In fp32 while that neither overflows nor loses
-// small values; else each square in fp64.
+// Sum of squares of one vector in fp32, and whether that neither overflowed nor
+// lost small values; where it did, the squares are taken again in fp64.
 template <typename T>
-__device__ __forceinline__ double squares(const uint4& raw) {
+__device__ __forceinline__ float squares(const uint4& raw) {
   const T* p = reinterpret_cast<const T*>(&raw);
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < Wide<T>::N; ++i) s = fmaf(to_f<T>(p[i]), to_f<T>(p[i]), s);
-  if (s > 1e-24f && s < 1e37f) return s;
-  double a = 0.0;
-#pragma unroll
-  for (int i = 0; i < Wide<T>::N; ++i) a += (double)to_f<T>(p[i]) * to_f<T>(p[i]);
-  return a;
+  return s;
 }
+__device__ __forceinline__ bool fits(float s) { return s > 1e-24f && s < 1e37f; }
 template <typename T>
 __device__ __forceinline__ double square1(T v) {
   const double x = to_f<T>(v);
@@ -80,13 +84,25 @@ __device__ double piece_squares(const Item& it, unsigned piece) {
   const int nv = (n - head) / N;
   const uint4* v = reinterpret_cast<const uint4*>(g + head);
   if ((int)threadIdx.x < head) a += square1<T>(g[threadIdx.x]);
-  constexpr int U = 4;
+  constexpr int U = 8;
   for (int i = threadIdx.x; i < nv; i += kThreads * U) {
     uint4 r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) r[u] = i + u * kThreads < nv ? v[i + u * kThreads] : uint4{0, 0, 0, 0};
+    float q[U];
+    bool all = true;
 #pragma unroll
-    for (int u = 0; u < U; ++u) a += squares<T>(r[u]);
+    for (int u = 0; u < U; ++u) {
+      q[u] = squares<T>(r[u]);
+      all = all && (fits(q[u]) || i + u * kThreads >= nv);
+    }
+    if (all) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) a += q[u];
+    } else {
+      for (int u = 0; u < U && i + u * kThreads < nv; ++u)
+        for (int e = 0; e < N; ++e) a += square1<T>(g[head + (long long)(i + u * kThreads) * N + e]);
+    }
   }
   for (int i = head + nv * N + threadIdx.x; i < n; i += kThreads) a += square1<T>(g[i]);
   return a;
@@ -113,11 +129,14 @@ __device__ __forceinline__ double partials_sum(const double* part, int n) {
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     grad_squares_kernel(const __grid_constant__ List<MAX> l, double* __restrict__ part) {
   double a = 0.0;
-  for (unsigned p = blockIdx.x; p < l.pieces; p += gridDim.x) {
-    const Item& it = l.t[find(l, p)];
+  const unsigned p0 = range_start(l.pieces, blockIdx.x), p1 = range_start(l.pieces, blockIdx.x + 1);
+  int i = p0 < p1 ? find(l, p0) : 0;
+  for (unsigned p = p0; p < p1; ++p) {
+    while (i + 1 < l.count && l.t[i + 1].first <= p) ++i;
+    const Item& it = l.t[i];
     a += it.act ? piece_squares<bf16>(it, p - it.first) : piece_squares<float>(it, p - it.first);
   }
   a = block_sum(a);
@@ -148,13 +167,13 @@ __device__ void piece_scale(const Item& it, unsigned piece, float scale) {
     uint4 r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i + u * kThreads < nv) r[u] = v[i + u * kThreads];
+      if (i + u * kThreads < nv) r[u] = __ldcs(v + i + u * kThreads);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       T* p = reinterpret_cast<T*>(&r[u]);
 #pragma unroll
       for (int e = 0; e < N; ++e) p[e] = from_f<T>(to_f<T>(p[e]) * scale);
-      if (i + u * kThreads < nv) w[i + u * kThreads] = r[u];
+      if (i + u * kThreads < nv) __stcs(w + i + u * kThreads, r[u]);
     }
   }
   for (int i = head + nv * N + threadIdx.x; i < n; i += kThreads)
@@ -162,17 +181,18 @@ __device__ void piece_scale(const Item& it, unsigned piece, float scale) {
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     grad_clip_kernel(const __grid_constant__ List<MAX> l, const double* __restrict__ part, int n,
                      float max_norm, float* __restrict__ norm) {
   const float total = (float)sqrt(partials_sum(part, n));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   const float c = max_norm / (total + 1e-6f);
   const float scale = c > 1.f ? 1.f : c;  // a NaN norm scales by NaN
-  // Last piece first: what the norm's pass read last is still in L2.
-  for (unsigned q = blockIdx.x; q < l.pieces; q += gridDim.x) {
-    const unsigned p = l.pieces - 1 - q;
-    const Item& it = l.t[find(l, p)];
+  const unsigned p0 = range_start(l.pieces, blockIdx.x), p1 = range_start(l.pieces, blockIdx.x + 1);
+  int i = p0 < p1 ? find(l, p1 - 1) : 0;
+  for (unsigned p = p1; p-- > p0;) {
+    while (l.t[i].first > p) --i;
+    const Item& it = l.t[i];
     if (scale == 1.f && it.g == it.out) continue;
     if (it.act)
       piece_scale<bf16>(it, p - it.first, scale);

@@ -71,6 +71,11 @@ ConvBytes conv_bytes(const ConvDims& d) {
                    (size_t)d.B * 4};
 }
 
+// Whether four channels at a time can be read and written as one vector.
+bool conv_vectors(const ConvDims& d, std::initializer_list<const void*> ps) {
+  return d.d % 4 == 0 && all_aligned(d.bf16_act ? 8 : 16, ps);
+}
+
 // ------------------------------------------------------------------ scan
 e2ttt_status ssm_dims(const char* who, const e2ttt_ssm_shape* s, SsmDims* d) {
   if (!s) return failf(E2TTT_ERR_INVALID_ARG, "%s: shape is NULL", who);
@@ -114,15 +119,17 @@ SsmBytes ssm_bytes(const SsmDims& d) {
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Forward scratch: status word, the chunks' decays, their logarithms (tensor
-// cores) and their states (in saved_states where given).
+// cores), their start states in bf16 (tensor cores) and their states (in
+// saved_states where given).
 struct SsmFwdWs {
-  size_t decay, logs, states, total;
+  size_t decay, logs, starts, states, total;
 };
 SsmFwdWs ssm_fwd_layout(const SsmDims& d) {
   SsmFwdWs L{};
   L.decay = 256;
   L.logs = L.decay + up256((size_t)d.NC * d.B * d.H * 4);
-  L.states = L.logs + (d.tc ? up256(ssm_tc_logs_bytes(d)) : 0);
+  L.starts = L.logs + (d.tc ? up256(ssm_tc_logs_bytes(d)) : 0);
+  L.states = L.starts + (d.tc ? up256(ssm_bytes(d).saved / 2) : 0);
   L.total = L.states + up256(ssm_bytes(d).saved);
   return L;
 }
@@ -206,7 +213,7 @@ e2ttt_status e2ttt_short_conv_fwd(const e2ttt_conv_shape* s, const void* x, cons
     TRY(check_spans(who, {{x, n.x, "x"}, {w, n.w, "w"}, {bias, n.b, "bias"}, {state, n.st, "state"},
                           {lengths, n.len, "lengths"}},
                     {{y, n.x, "y"}, {state_end, n.st, "state_end"}}));
-    const bool vec = d.d % (d.bf16_act ? 8 : 4) == 0 && all_aligned16({x, state, y, state_end});
+    const bool vec = conv_vectors(d, {x, state, y, state_end});
     ConvArgs a{d, x, w, bias, state, lengths, vec, (cudaStream_t)stream};
     return check_run(conv_fwd(a, y, d.W > 1 ? state_end : nullptr), who);
   })
@@ -234,7 +241,7 @@ e2ttt_status e2ttt_short_conv_bwd(const e2ttt_conv_shape* s, const void* x, cons
                           {lengths, n.len, "lengths"}, {dy, n.x, "dy"}, {dstate_end, n.st, "dstate_end"}},
                     {{dx, n.x, "dx"}, {dw, n.w, "dw"}, {dbias, n.b, "dbias"}, {dstate, n.st, "dstate"},
                      {ws, need, "workspace"}}));
-    const bool vec = d.d % (d.bf16_act ? 8 : 4) == 0 && all_aligned16({x, state, dy, dstate_end, dx, dstate});
+    const bool vec = conv_vectors(d, {x, state, dy, dstate_end, dx, dstate});
     ConvArgs a{d, x, w, bias, state, lengths, vec, (cudaStream_t)stream};
     return check_run(conv_bwd(a, dy, d.W > 1 ? dstate_end : nullptr, dx, dw, dbias,
                               d.W > 1 ? dstate : nullptr, ws), who);
@@ -255,7 +262,7 @@ e2ttt_status e2ttt_short_conv_step(const e2ttt_conv_shape* s, const void* x, con
     TRY(check_aligned(who, 4, {{w, 0, "w"}, {bias, 0, "bias"}}));
     TRY(check_spans(who, {{x, n.x, "x"}, {w, n.w, "w"}, {bias, n.b, "bias"}},
                     {{state, n.st, "state"}, {y, n.x, "y"}}));
-    const bool vec = d.d % (d.bf16_act ? 8 : 4) == 0 && all_aligned16({x, state, y});
+    const bool vec = conv_vectors(d, {x, state, y});
     ConvArgs a{d, x, w, bias, nullptr, nullptr, vec, (cudaStream_t)stream};
     return check_run(conv_step(a, state, y), who);
   })
@@ -296,7 +303,8 @@ e2ttt_status e2ttt_ssm_scan_fwd(const e2ttt_ssm_shape* s, const void* q, const v
                      {ws, need, "workspace"}}));
     char* w = (char*)ws;
     SsmFwdArgs a{d, q, k, v, dt, A, D, S0, lengths, y, S_end, saved ? saved : (float*)(w + lay.states),
-                 (float*)(w + lay.decay), (float*)(w + lay.logs), (int*)w, (cudaStream_t)stream};
+                 (float*)(w + lay.decay), (float*)(w + lay.logs), w + lay.starts, saved != nullptr, (int*)w,
+                 (cudaStream_t)stream};
     return check_run(d.tc ? ssm_tc_fwd(a) : ssm_fwd(a), who);
   })
 }

@@ -24,7 +24,7 @@ struct ConvArgs {
   const float *w, *bias;  // bias may be NULL
   const void* state;      // may be NULL: zeros
   const int* lengths;     // may be NULL: T everywhere
-  bool vec;               // 16-byte vectors apply: row size and every pointer
+  bool vec;               // vectors of 4 channels apply: row size and every pointer
   cudaStream_t st;
 };
 size_t conv_bwd_workspace_bytes(const ConvDims& s);
@@ -55,6 +55,8 @@ struct SsmFwdArgs {
   float* states;  // [NC][B*H][P][N]: saved_states or workspace
   float* decay;   // [NC][B*H] workspace
   float* logs;    // tensor cores: the chunks' logarithms, workspace
+  void* starts;   // tensor cores: the chunks' start states in bf16, workspace
+  bool keep;      // the fp32 states are wanted (saved_states)
   int* status;    // device status word of the bounded waits
   cudaStream_t st;
 };
@@ -62,9 +64,10 @@ cudaError_t ssm_fwd(const SsmFwdArgs& a);     // CUDA cores, any shape
 cudaError_t ssm_tc_fwd(const SsmFwdArgs& a);  // tensor cores, shapes with tc set
 size_t ssm_tc_logs_bytes(const SsmDims& s);
 // The states' passage along the chunks (back: their adjoint's, from the end),
-// from `first` (NULL: zero); what is left after the last chunk goes to `last`.
+// from `first` (NULL: zero); what is left after the last chunk goes to `last`, a
+// bf16 copy of the states to `copy` (may be NULL); without `keep` only that.
 cudaError_t ssm_carry(const SsmDims& s, bool back, const float* first, const float* decay,
-                      float* states, float* last, cudaStream_t st);
+                      float* states, float* last, void* copy, bool keep, cudaStream_t st);
 
 struct SsmBwdArgs {
   SsmDims s;

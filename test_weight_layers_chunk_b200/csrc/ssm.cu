@@ -133,8 +133,15 @@ __global__ void __launch_bounds__(kT)
 
 // Turns the chunks' own contributions into the states at their starts (REV 0,
 // from `first`) or the gradients at their ends (REV 1, from the last chunk
-// back); `last` gets what is left after the last one. Elementwise along the
-// chunks, bound by the states' bytes; V is float4 where rows and pointers allow.
+// back); `last` gets what is left after the last one. `copy`, where given, takes
+// them rounded to bf16 (what the outputs' products read), and without `keep` the
+// fp32 ones are not written. Elementwise along the chunks, bound by the states'
+// bytes; V is float4 where rows and pointers allow.
+__device__ __forceinline__ void store_bf16(bf16* p, float x) { *p = from_f<bf16>(x); }
+__device__ __forceinline__ void store_bf16(bf16* p, const float4& x) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  *reinterpret_cast<uint2*>(p) = uint2{*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b)};
+}
 __device__ __forceinline__ void decay_add(float& run, float d, float own) { run = fmaf(d, run, own); }
 __device__ __forceinline__ void decay_add(float4& run, float d, const float4& own) {
   run = float4{fmaf(d, run.x, own.x), fmaf(d, run.y, own.y), fmaf(d, run.z, own.z), fmaf(d, run.w, own.w)};
@@ -142,7 +149,9 @@ __device__ __forceinline__ void decay_add(float4& run, float d, const float4& ow
 template <typename V, int REV>
 __global__ void __launch_bounds__(kT)
     carry_kernel(int NC, int BH, long long PN, const V* __restrict__ first,
-                 const float* __restrict__ decay, V* __restrict__ states, V* __restrict__ last) {
+                 const float* __restrict__ decay, V* __restrict__ states, V* __restrict__ last,
+                 bf16* __restrict__ copy, bool keep) {
+  constexpr int W = sizeof(V) / sizeof(float);
   const int bh = blockIdx.y;
   const long long i = (long long)blockIdx.x * kT + threadIdx.x;
   griddep_wait();
@@ -165,7 +174,9 @@ __global__ void __launch_bounds__(kT)
     for (int u = 0; u < U; ++u) {
       const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
       if (c0 + u < NC) {
-        states[((long long)c * BH + bh) * PN + i] = run;
+        const long long at = ((long long)c * BH + bh) * PN + i;
+        if (keep) states[at] = run;
+        if (copy) store_bf16(copy + at * W, run);
         decay_add(run, d[u], own[u]);
       }
     }
@@ -492,32 +503,85 @@ __global__ void __launch_bounds__(kT) head_sum_kernel(const float* __restrict__ 
 }
 
 // One token: S = e^{dt A} S + dt v k^T in place, y = S q + D v. Bound by HBM: S
-// is read and written once. Eight lanes share a state row, so a warp reads four
-// rows' 128-byte lines at a time.
+// is read and written once. kLanes lanes share a state row; each loads all its
+// pieces of the row before it stores any, so that a warp has whole rows in flight.
+//   VEC: 8 lanes a row and PIECES float4 a lane (N <= 32 PIECES, a multiple of 4)
+//   else 32 lanes a row, single values
 template <typename T>
+__device__ __forceinline__ void load4(const T* p, float (&f)[4]);
+template <>
+__device__ __forceinline__ void load4<float>(const float* p, float (&f)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+template <>
+__device__ __forceinline__ void load4<bf16>(const bf16* p, float (&f)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
+  f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+template <typename T, int PIECES>  // PIECES 0: single values
 __global__ void __launch_bounds__(kT)
     ssm_step_kernel(SsmDims s, const T* __restrict__ q, const T* __restrict__ k,
                     const T* __restrict__ v, const float* __restrict__ dt,
                     const float* __restrict__ A, const float* __restrict__ D,
                     float* __restrict__ S, T* __restrict__ y) {
+  constexpr int kLanes = PIECES ? 8 : 32;
   const int bh = blockIdx.y, b = bh / s.H, h = bh - b * s.H, g = h / (s.H / s.G);
-  const int p = blockIdx.x * (kT / 8) + threadIdx.x / 8, l = threadIdx.x & 7;
+  const int p = blockIdx.x * (kT / kLanes) + threadIdx.x / kLanes, l = threadIdx.x % kLanes;
   const bool on = p < s.P;
-  const float e = dt[bh], dec = ex2(e * A[h] * 1.44269504f);
-  const float x = on ? to_f<T>(v[(long long)bh * s.P + p]) : 0.f;
+  float* row = S + ((long long)bh * s.P + p) * s.N;
   const T* qr = q + ((long long)b * s.G + g) * s.N;
   const T* kr = k + ((long long)b * s.G + g) * s.N;
-  float* row = S + ((long long)bh * s.P + p) * s.N;
-  const float ex = e * x;
-  float acc = 0.f;
-  if (on)
-    for (int n = l; n < s.N; n += 8) {
-      const float u = fmaf(dec, row[n], ex * to_f<T>(kr[n]));
-      row[n] = u;
-      acc = fmaf(u, to_f<T>(qr[n]), acc);
-    }
+  float acc = 0.f, x = 0.f;
+  if constexpr (PIECES > 0) {
+    float4 r[PIECES];
 #pragma unroll
-  for (int o = 4; o; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
+    for (int i = 0; i < PIECES; ++i) {
+      const int n = (i * kLanes + l) * 4;
+      if (on && n < s.N) r[i] = __ldcs(reinterpret_cast<const float4*>(row + n));
+    }
+    const float e = dt[bh], dec = ex2(e * A[h] * 1.44269504f);
+    x = on ? to_f<T>(v[(long long)bh * s.P + p]) : 0.f;
+    const float ex = e * x;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int n = (i * kLanes + l) * 4;
+      if (on && n < s.N) {
+        float kf[4], qf[4];
+        load4<T>(kr + n, kf);
+        load4<T>(qr + n, qf);
+        r[i].x = fmaf(dec, r[i].x, ex * kf[0]);
+        r[i].y = fmaf(dec, r[i].y, ex * kf[1]);
+        r[i].z = fmaf(dec, r[i].z, ex * kf[2]);
+        r[i].w = fmaf(dec, r[i].w, ex * kf[3]);
+        __stcs(reinterpret_cast<float4*>(row + n), r[i]);
+        acc = fmaf(r[i].x, qf[0], acc);
+        acc = fmaf(r[i].y, qf[1], acc);
+        acc = fmaf(r[i].z, qf[2], acc);
+        acc = fmaf(r[i].w, qf[3], acc);
+      }
+    }
+  } else {
+    const float e = dt[bh], dec = ex2(e * A[h] * 1.44269504f);
+    x = on ? to_f<T>(v[(long long)bh * s.P + p]) : 0.f;
+    const float ex = e * x;
+    float r[8];  // N <= 256
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (on && i * 32 + l < s.N) r[i] = row[i * 32 + l];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = i * 32 + l;
+      if (on && n < s.N) {
+        r[i] = fmaf(dec, r[i], ex * to_f<T>(kr[n]));
+        row[n] = r[i];
+        acc = fmaf(r[i], to_f<T>(qr[n]), acc);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
   if (on && l == 0) y[(long long)bh * s.P + p] = from_f<T>(D ? fmaf(D[h], x, acc) : acc);
 }
 
@@ -578,7 +642,7 @@ cudaError_t fwd_t(const SsmFwdArgs& a) {
         s, (const T*)a.v, (const T*)a.k, a.dt, a.A, a.lengths, a.states, a.decay, a.status);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, a.st)) != cudaSuccess) return e;
+  if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, nullptr, true, a.st)) != cudaSuccess) return e;
   E2TTT_TRACE("ssm_chunk_out", a.st);
   auto kern = chunk_out_kernel<T, 2>;
   if constexpr (std::is_same<T, float>::value)  // bf16 with so few columns runs on the tensor cores
@@ -601,7 +665,7 @@ cudaError_t bwd_t(const SsmBwdArgs& a, const SsmBwdScratch& w) {
         s, (const T*)a.dy, (const T*)a.q, a.dt, a.A, a.lengths, w.ends, w.decay, w.status);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, a.st)) != cudaSuccess) return e;
+  if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, nullptr, true, a.st)) != cudaSuccess) return e;
   {
     E2TTT_TRACE("ssm_chunk_grad", a.st);
     auto kern = chunk_grad_kernel<T, 2>;
@@ -619,18 +683,18 @@ cudaError_t bwd_t(const SsmBwdArgs& a, const SsmBwdScratch& w) {
 }  // namespace
 
 cudaError_t ssm_carry(const SsmDims& s, bool back, const float* first, const float* decay,
-                      float* states, float* last, cudaStream_t st) {
+                      float* states, float* last, void* copy, bool keep, cudaStream_t st) {
   const int BH = s.B * s.H;
   const long long PN = (long long)s.P * s.N;
   E2TTT_TRACE(back ? "ssm_carry_back" : "ssm_carry", st);
   if (PN % 4 == 0 && !(((uintptr_t)first | (uintptr_t)states | (uintptr_t)last) & 15)) {
     const dim3 grid((unsigned)((PN / 4 + kT - 1) / kT), BH);
     return launch_pdl(back ? carry_kernel<float4, 1> : carry_kernel<float4, 0>, grid, dim3(kT), 0, st, s.NC, BH,
-                      PN / 4, (const float4*)first, decay, (float4*)states, (float4*)last);
+                      PN / 4, (const float4*)first, decay, (float4*)states, (float4*)last, (bf16*)copy, keep);
   }
   const dim3 grid((unsigned)((PN + kT - 1) / kT), BH);
   return launch_pdl(back ? carry_kernel<float, 1> : carry_kernel<float, 0>, grid, dim3(kT), 0, st, s.NC, BH, PN,
-                    first, decay, states, last);
+                    first, decay, states, last, (bf16*)copy, keep);
 }
 
 cudaError_t ssm_grad_sums(const SsmBwdArgs& a, const SsmBwdScratch& w, int parts) {
@@ -670,17 +734,22 @@ cudaError_t ssm_bwd(const SsmBwdArgs& a) {
   return a.s.bf16_act ? bwd_t<bf16>(a, w) : bwd_t<float>(a, w);
 }
 
-cudaError_t ssm_step(const SsmStepArgs& a) {
+template <typename T>
+static cudaError_t step_t(const SsmStepArgs& a) {
   const SsmDims& s = a.s;
-  const dim3 grid((s.P + kT / 8 - 1) / (kT / 8), s.B * s.H);
+  const uintptr_t qk = (uintptr_t)a.q | (uintptr_t)a.k;
+  const bool vec = s.N % 4 == 0 && !((uintptr_t)a.S & 15) && !(qk & (4 * sizeof(T) - 1));
+  const int pieces = !vec ? 0 : s.N <= 64 ? 2 : s.N <= 128 ? 4 : 8;
+  auto kern = pieces == 0   ? ssm_step_kernel<T, 0>
+              : pieces == 2 ? ssm_step_kernel<T, 2>
+              : pieces == 4 ? ssm_step_kernel<T, 4>
+                            : ssm_step_kernel<T, 8>;
+  const int rows = kT / (vec ? 8 : 32);
   E2TTT_TRACE("ssm_step", a.st);
-  if (s.bf16_act)
-    ssm_step_kernel<bf16><<<grid, kT, 0, a.st>>>(s, (const bf16*)a.q, (const bf16*)a.k,
-                                                 (const bf16*)a.v, a.dt, a.A, a.D, a.S, (bf16*)a.y);
-  else
-    ssm_step_kernel<float><<<grid, kT, 0, a.st>>>(s, (const float*)a.q, (const float*)a.k,
-                                                  (const float*)a.v, a.dt, a.A, a.D, a.S, (float*)a.y);
+  kern<<<dim3((s.P + rows - 1) / rows, s.B * s.H), kT, 0, a.st>>>(
+      s, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.dt, a.A, a.D, a.S, (T*)a.y);
   return cudaGetLastError();
 }
+cudaError_t ssm_step(const SsmStepArgs& a) { return a.s.bf16_act ? step_t<bf16>(a) : step_t<float>(a); }
 
 }  // namespace e2ttt

@@ -95,21 +95,25 @@ __device__ __forceinline__ uint4 load8(const bf16* row, int c, int cols) {
   return r;
 }
 
-// Rows [0, n) of src (pitch ld, `cols` columns) into a tile of kQ rows and
-// `blocks` 64-column blocks; everything else is zero. vec: 16-byte copies apply.
-__device__ __forceinline__ void load_rows(uint8_t* tile, int blocks, const bf16* src, long long ld, int n,
-                                          int cols, bool vec) {
-  const uint32_t base = smem_u32(tile);
-  const int per = blocks * 8;
-  for (int i = threadIdx.x; i < kQ * per; i += kThreads) {
-    const int r = i / per, j = i - r * per;
-    const bool on = r < n && j * 8 < cols;
-    const uint32_t at = piece<kQ>(r, j);
-    if (vec)
-      cp16(base + at, on ? src + (long long)r * ld + j * 8 : src, on);
+// Rows [0, n) of src (pitch ld, `cols` columns) into a tile of ROWS rows and
+// BLOCKS 64-column blocks; everything else is zero. VEC: 16-byte copies apply.
+template <int ROWS, int BLOCKS, bool VEC>
+__device__ __forceinline__ void load_rows(uint8_t* tile, const bf16* src, long long ld, int n, int cols) {
+  constexpr int kPer = BLOCKS * 8, kStep = kThreads / kPer;  // pieces in a row, rows at a time
+  static_assert(kStep % 8 == 0 && ROWS % kStep == 0, "a thread's rows share their swizzle");
+  const int j = threadIdx.x % kPer, r0 = threadIdx.x / kPer;
+  const int left = j * 8 < cols ? n - r0 : 0;
+  const bf16* p = src + r0 * ld + j * 8;
+  uint8_t* dst = tile + piece<ROWS>(r0, j);
+#pragma unroll
+  for (int i = 0; i < ROWS / kStep; ++i) {
+    const bool on = i * kStep < left;
+    if constexpr (VEC)
+      cp16(smem_u32(dst) + i * kStep * 128, on ? p : src, on);
     else
-      *reinterpret_cast<uint4*>(tile + at) =
-          on ? load8(src + (long long)r * ld, j * 8, cols) : uint4{0, 0, 0, 0};
+      *reinterpret_cast<uint4*>(dst + i * kStep * 128) =
+          on ? load8(src + (long long)(r0 + i * kStep) * ld, j * 8, cols) : uint4{0, 0, 0, 0};
+    p += kStep * ld;
   }
 }
 
@@ -122,13 +126,33 @@ __device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 
 __device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 // Eight values to a row of which `left` columns remain.
-__device__ __forceinline__ void store8(bf16* out, const uint4& w, int left, bool vec) {
-  if (vec && left >= 8) {
-    *reinterpret_cast<uint4*>(out) = w;
+template <bool VEC>
+__device__ __forceinline__ void store8(bf16* out, const uint4& w, int left) {
+  if constexpr (VEC) {
+    if (left >= 8) *reinterpret_cast<uint4*>(out) = w;  // rows are whole pieces
   } else {
     const bf16* e = reinterpret_cast<const bf16*>(&w);
     for (int j = 0; j < 8 && j < left; ++j) out[j] = e[j];
   }
+}
+
+// Eight fp32 values of a row of which `left` remain (at most 0: none), zeros beyond.
+template <bool VEC>
+__device__ __forceinline__ void load8f(float (&f)[8], const float* p, int left) {
+  if constexpr (VEC) {  // rows are whole pieces
+    float4 a{0, 0, 0, 0}, b{0, 0, 0, 0};
+    if (left > 0) {
+      a = *reinterpret_cast<const float4*>(p);
+      b = *reinterpret_cast<const float4*>(p + 4);
+    }
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = e < left ? p[e] : 0.f;
+  }
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // f as three bf16 terms: f = t0 + t1 + t2 to 24 bits.
@@ -232,11 +256,11 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
 // w_s = e^{c_Q-c_s} eta_s; with REV 1 x = dy, y = q, w_t = e^{c_t}. D[n][p] on
 // the tensor cores (128 state columns as rows of the tile): y contracted over
 // its rows, w x in three terms.
-template <int REV>
+template <int REV, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2)
     state_kernel(SsmDims s, const bf16* __restrict__ x, const bf16* __restrict__ y,
                  const float* __restrict__ logs, const int* __restrict__ lengths,
-                 float* __restrict__ states, int* __restrict__ status, bool vec) {
+                 float* __restrict__ states, int* __restrict__ status) {
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[3 * kQ];
   __shared__ uint64_t bar;
@@ -250,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_wait();
   griddep_launch_dependents();
   const int n = min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ);
-  load_rows(ys, 2, y + (((long long)b * s.G + g) * s.T + t0) * s.N, s.N, n, s.N, vec);
+  load_rows<kQ, 2, VEC>(ys, y + (((long long)b * s.G + g) * s.T + t0) * s.N, s.N, n, s.N);
   load_logs(L, logs, bh, s.NC, c);
   const int r = threadIdx.x >> 1, j0 = (threadIdx.x & 1) * 4;
   const bf16* xr = x + ((long long)bh * s.T + t0 + r) * s.P + p0;
@@ -259,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int j = 0; j < 4; ++j) {
     const int col = (j0 + j) * 8;
     xv[j] = uint4{0, 0, 0, 0};
-    if (r < n && col < np) xv[j] = vec ? *reinterpret_cast<const uint4*>(xr + col) : load8(xr, col, np);
+    if (r < n && col < np) xv[j] = VEC ? *reinterpret_cast<const uint4*>(xr + col) : load8(xr, col, np);
   }
   __syncthreads();
   const float w = REV ? L.from_start(r) : L.to_end(r) * L.eta[r];
@@ -304,18 +328,18 @@ __global__ void __launch_bounds__(kThreads, 2)
 // block: exactly within the row's own block, and as e^{c_t - c_r} e^{c_r - c_s}
 // with r the last token of an earlier block (two factors that are both at most
 // one for a decaying state), so that only a quarter of them takes an exponential
-// each. `tail[s]` holds e^{c_r - c_s}.
-__device__ __forceinline__ void fill_tails(const ChunkLogs& L, float* tail) {
-  if (threadIdx.x < kQ) tail[threadIdx.x] = L.decay(threadIdx.x | 31, threadIdx.x);
+// each. `tail[s]` holds e^{c_r - c_s} (times eta_s where asked).
+__device__ __forceinline__ void fill_tails(const ChunkLogs& L, float* tail, bool with_eta) {
+  if (threadIdx.x < kQ)
+    tail[threadIdx.x] = L.decay(threadIdx.x | 31, threadIdx.x) * (with_eta ? L.eta[threadIdx.x] : 1.f);
 }
 
-template <int NB>
+template <int NB, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2)
     out_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,
                const bf16* __restrict__ v, const float* __restrict__ logs,
                const float* __restrict__ D, const int* __restrict__ lengths,
-               const float* __restrict__ states, bf16* __restrict__ y, int* __restrict__ status,
-               bool vec) {
+               const bf16* __restrict__ states, bf16* __restrict__ y, int* __restrict__ status) {
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[3 * kQ];
   __shared__ float tail[kQ];
@@ -333,19 +357,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_launch_dependents();
   const int n = min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ);
   const long long qo = (((long long)b * s.G + g) * s.T + t0) * s.N;
-  load_rows(qs, NB, q + qo, s.N, n, s.N, vec);
-  load_rows(ks, NB, k + qo, s.N, n, s.N, vec);
-  load_rows(vs, 1, v + ((long long)bh * s.T + t0) * s.P + p0, s.P, n, np, vec);
+  load_rows<kQ, NB, VEC>(qs, q + qo, s.N, n, s.N);
+  load_rows<kQ, NB, VEC>(ks, k + qo, s.N, n, s.N);
+  load_rows<kPT, NB, VEC>(Ss, states + (((long long)c * s.B * s.H + bh) * s.P + p0) * s.N, s.N, np, s.N);
+  load_rows<kQ, 1, VEC>(vs, v + ((long long)bh * s.T + t0) * s.P + p0, s.P, n, np);
   load_logs(L, logs, bh, s.NC, c);
-  const float* S = states + (((long long)c * s.B * s.H + bh) * s.P + p0) * s.N;
-  for (int i = threadIdx.x; i < kPT * NB * 8; i += kThreads) {
-    const int p = i / (NB * 8), j = i - p * (NB * 8);
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = p < np && j * 8 + e < s.N ? S[(long long)p * s.N + j * 8 + e] : 0.f;
-    *reinterpret_cast<uint4*>(Ss + piece<kPT>(p, j)) =
-        uint4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
-  }
   cp_wait();
   publish();
   const int nsteps = (s.N + 15) / 16;
@@ -356,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     mma<kQ, false, kPT, false, 64>(tmem + kYi, qs, Ss, nsteps, false);
     tc::mma_commit(&bar);
   }
-  fill_tails(L, tail);
+  fill_tails(L, tail, true);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = warp >> 2;
   const int t = quad * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 32; ++i) {
           const int u = cb * 32 + i;
           if (cb < quad)
-            m[i] *= row * tail[u] * L.eta[u];
+            m[i] *= row * tail[u];
           else
             m[i] = u <= t ? m[i] * (L.decay(t, u) * L.eta[u]) : 0.f;
         }
@@ -411,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float y1 = fmaf(f, yi[a + 1], yd[a + 1]) + Dh * hi_f(xu[e]);
             ou[e] = t < n ? pack2(y0, y1) : 0u;
           }
-          store8(out + i * 8, o, np - (half * 32 + i * 8), vec);
+          store8<VEC>(out + i * 8, o, np - (half * 32 + i * 8));
         }
     }
   }
@@ -472,14 +488,14 @@ struct GradOut {
 //   two parts of dv), [256, 384) dq, [384, 512) dk
 //   shared memory: q, k; v, dy of the item; S and X in three terms, later
 //   overwritten by the two score matrices (X's first term stays)
-template <int NB>
+template <int NB, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     grad_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,
                 const bf16* __restrict__ v, const bf16* __restrict__ dy,
                 const float* __restrict__ logs, const float* __restrict__ A,
                 const float* __restrict__ D, const int* __restrict__ lengths,
                 const float* __restrict__ states, const float* __restrict__ ends, GradOut o,
-                int per, int* __restrict__ status, bool vec) {
+                int per, int* __restrict__ status) {
   constexpr int kTerm = NB * kPT * 128;  // bytes of one term of a state
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[3 * kQ];
@@ -502,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   const int n = min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ);
   const long long qo = ((long long)bg * s.T + t0) * s.N;
-  load_rows(qs, NB, q + qo, s.N, n, s.N, vec);
-  load_rows(ks, NB, k + qo, s.N, n, s.N, vec);
+  load_rows<kQ, NB, VEC>(qs, q + qo, s.N, n, s.N);
+  load_rows<kQ, NB, VEC>(ks, k + qo, s.N, n, s.N);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = warp >> 2;
   const int t = quad * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -522,41 +538,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = g * HG + it / s.NPT, pt = it % s.NPT, bh = b * s.H + h;
     const int p0 = pt * kPT, np = min(kPT, s.P - p0);
     const long long vo = ((long long)bh * s.T + t0) * s.P + p0;
-    load_rows(vs, 1, v + vo, s.P, n, np, vec);
-    load_rows(gs, 1, dy + vo, s.P, n, np, vec);
+    load_rows<kQ, 1, VEC>(vs, v + vo, s.P, n, np);
+    load_rows<kQ, 1, VEC>(gs, dy + vo, s.P, n, np);
     load_logs(L, logs, bh, s.NC, c);
-    // S and X, as three terms each, and <S, X>
+    // S and X, as three terms each, and <S, X>: two batches of loads, so that a
+    // batch is in flight at once
     {
+      constexpr int kPer = NB * 8, kStep = kThreads / kPer, kIt = kPT / kStep;
       const long long so = (((long long)c * BH + bh) * s.P + p0) * s.N;
+      const int j = threadIdx.x % kPer, r0 = threadIdx.x / kPer;
       float ip = 0.f;
-      for (int i = threadIdx.x; i < kPT * NB * 8; i += kThreads) {
-        const int p = i / (NB * 8), j = i - p * (NB * 8);
-        float f[8], x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool in = p < np && j * 8 + e < s.N;
-          const long long at = so + (long long)p * s.N + j * 8 + e;
-          f[e] = in ? states[at] : 0.f;
-          x[e] = in ? ends[at] : 0.f;
+      for (int i0 = 0; i0 < kIt; i0 += 2) {
+        float f[2][8], x[2][8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int p = r0 + (i0 + i) * kStep;
+          load8f<VEC>(f[i], states + so + (long long)p * s.N + j * 8, p < np ? s.N - j * 8 : 0);
+          load8f<VEC>(x[i], ends + so + (long long)p * s.N + j * 8, p < np ? s.N - j * 8 : 0);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ip = fmaf(f[e], x[e], ip);
-        const uint32_t at = piece<kPT>(p, j);
-        uint4 term[3];
-        split3(f, term);
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4*>(St + m * kTerm + at) = term[m];
-        split3(x, term);
-        *reinterpret_cast<uint4*>(Xs + at) = term[0];
-        *reinterpret_cast<uint4*>(St + 3 * kTerm + at) = term[1];
-        if constexpr (NB == 1)
-          *reinterpret_cast<uint4*>(St + 4 * kTerm + at) = term[2];
-        else
-          *reinterpret_cast<uint4*>(Xs + kTerm + at) = term[2];
+          for (int e = 0; e < 8; ++e) ip = fmaf(f[i][e], x[i][e], ip);
+          const uint32_t at = piece<kPT>(r0 + (i0 + i) * kStep, j);
+          uint4 term[3];
+          split3(f[i], term);
+#pragma unroll
+          for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4*>(St + m * kTerm + at) = term[m];
+          split3(x[i], term);
+          *reinterpret_cast<uint4*>(Xs + at) = term[0];
+          *reinterpret_cast<uint4*>(St + 3 * kTerm + at) = term[1];
+          *reinterpret_cast<uint4*>((NB == 1 ? St + 4 * kTerm : Xs + kTerm) + at) = term[2];
+        }
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) ip += __shfl_xor_sync(~0u, ip, d);
       if (lane == 0) warp_ip[warp] = ip;
+    }
+    if (it + 1 < i1) {
+      // the next item's rows and states into L2 while this one computes
+      const int h2 = g * HG + (it + 1) / s.NPT, q0 = (it + 1) % s.NPT * kPT, bh2 = b * s.H + h2;
+      const long long v2 = ((long long)bh2 * s.T + t0) * s.P + q0;
+      const long long s2 = (((long long)c * BH + bh2) * s.P + q0) * s.N;
+      const int room = min(kPT, s.P - q0);
+      if (threadIdx.x < n) prefetch_l2(v + v2 + (long long)threadIdx.x * s.P);
+      if (threadIdx.x >= 128 && threadIdx.x - 128 < n) prefetch_l2(dy + v2 + (long long)(threadIdx.x - 128) * s.P);
+      const int line = threadIdx.x * 32;  // of the tile's room * N values
+      if (line < room * s.N) {
+        prefetch_l2(states + s2 + line);
+        prefetch_l2(ends + s2 + line);
+      }
     }
     cp_wait();
     publish();
@@ -568,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, x2, kPT / 16, true);
       tc::mma_commit(&bar);
     }
-    fill_tails(L, tail);
+    fill_tails(L, tail, false);
     if (!(ok = done.wait())) break;
     // the states' parts of dq and dk, and their dots with q and k
     {
@@ -742,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float d1 = fmaf(eta, fmaf(e, a2[x + 1], a1[x + 1]), Dh * hi_f(u[j]));
             wu[j] = t < n ? pack2(d0, d1) : 0u;
           }
-          store8(out + i * 8, w, np - (half * 32 + i * 8), vec);
+          store8<VEC>(out + i * 8, w, np - (half * 32 + i * 8));
         }
     }
     tc::tc_fence_before();
@@ -766,10 +798,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           bf16* out = (which ? o.dk16 : o.dq16) + qo + (long long)t * s.N + col;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            store8(out + i * 8,
+            store8<VEC>(out + i * 8,
                    uint4{pack2(a[i * 8], a[i * 8 + 1]), pack2(a[i * 8 + 2], a[i * 8 + 3]),
                          pack2(a[i * 8 + 4], a[i * 8 + 5]), pack2(a[i * 8 + 6], a[i * 8 + 7])},
-                   s.N - col - i * 8, vec);
+                   s.N - col - i * 8);
         } else {
           float* out = (which ? o.dk : o.dq) + (((long long)bg * parts + split) * s.T + t0 + t) * s.N + col;
           if (s.N % 4 == 0) {
@@ -841,7 +873,7 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
   const int BH = s.B * s.H, parts = grad_parts(s);
   const long long items = (long long)s.H / s.G * s.NPT;
   const int per = (int)((items + parts - 1) / parts);
-  const bool vec = vectors(s, {a.q, a.k, a.v, a.dy, a.dq, a.dk, a.dv});
+  const bool vec = vectors(s, {a.q, a.k, a.v, a.dy, a.dq, a.dk, a.dv, a.states});
   cudaError_t e;
   {
     E2TTT_TRACE("ssm_logs", a.st);
@@ -851,21 +883,23 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
   }
   {
     E2TTT_TRACE("ssm_chunk_dstate", a.st);
-    if ((e = allow_smem(state_kernel<1>, state_smem())) != cudaSuccess) return e;
-    e = launch_pdl(state_kernel<1>, dim3(s.NC, BH, s.NPT), dim3(kThreads), state_smem(), a.st, s,
-                   (const bf16*)a.dy, (const bf16*)a.q, (const float*)w.logs, a.lengths, w.ends, w.status, vec);
+    auto kern = vec ? state_kernel<1, true> : state_kernel<1, false>;
+    if ((e = allow_smem(kern, state_smem())) != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(s.NC, BH, s.NPT), dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.dy,
+                   (const bf16*)a.q, (const float*)w.logs, a.lengths, w.ends, w.status);
     if (e != cudaSuccess) return e;
   }
-  if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, a.st)) != cudaSuccess) return e;
+  if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, nullptr, true, a.st)) != cudaSuccess) return e;
   {
     E2TTT_TRACE("ssm_chunk_grad", a.st);
-    auto kern = s.N <= 64 ? grad_kernel<1> : grad_kernel<2>;
+    auto kern = s.N <= 64 ? (vec ? grad_kernel<1, true> : grad_kernel<1, false>)
+                          : (vec ? grad_kernel<2, true> : grad_kernel<2, false>);
     const size_t smem = s.N <= 64 ? grad_smem<1>() : grad_smem<2>();
     if ((e = allow_smem(kern, smem)) != cudaSuccess) return e;
     const GradOut o{w.dq, w.dk, (bf16*)a.dq, (bf16*)a.dk, (bf16*)a.dv, w.ddt, w.dA, w.dD};
     e = launch_pdl(kern, dim3(s.NC, s.B * s.G, parts), dim3(kThreads), smem, a.st, s, (const bf16*)a.q,
                    (const bf16*)a.k, (const bf16*)a.v, (const bf16*)a.dy, (const float*)w.logs, a.A, a.D, a.lengths,
-                   a.states, (const float*)w.ends, o, per, w.status, vec);
+                   a.states, (const float*)w.ends, o, per, w.status);
     if (e != cudaSuccess) return e;
   }
   return ssm_grad_sums(a, w, parts);
@@ -885,19 +919,21 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
   }
   {
     E2TTT_TRACE("ssm_chunk_state", a.st);
-    if ((e = allow_smem(state_kernel<0>, state_smem())) != cudaSuccess) return e;
-    e = launch_pdl(state_kernel<0>, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.v,
-                   (const bf16*)a.k, (const float*)a.logs, a.lengths, a.states, a.status, vec);
+    auto kern = vec ? state_kernel<0, true> : state_kernel<0, false>;
+    if ((e = allow_smem(kern, state_smem())) != cudaSuccess) return e;
+    e = launch_pdl(kern, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.v, (const bf16*)a.k,
+                   (const float*)a.logs, a.lengths, a.states, a.status);
     if (e != cudaSuccess) return e;
   }
-  if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, a.st)) != cudaSuccess) return e;
+  if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, a.starts, a.keep, a.st)) != cudaSuccess) return e;
   E2TTT_TRACE("ssm_chunk_out", a.st);
-  auto kern = s.N <= 64 ? out_kernel<1> : out_kernel<2>;
+  auto kern = s.N <= 64 ? (vec ? out_kernel<1, true> : out_kernel<1, false>)
+                        : (vec ? out_kernel<2, true> : out_kernel<2, false>);
   const size_t smem = s.N <= 64 ? out_smem<1>() : out_smem<2>();
   if ((e = allow_smem(kern, smem)) != cudaSuccess) return e;
   return launch_pdl(kern, grid, dim3(kThreads), smem, a.st, s, (const bf16*)a.q, (const bf16*)a.k,
-                    (const bf16*)a.v, (const float*)a.logs, a.D, a.lengths, (const float*)a.states,
-                    (bf16*)a.y, a.status, vec);
+                    (const bf16*)a.v, (const float*)a.logs, a.D, a.lengths, (const bf16*)a.starts,
+                    (bf16*)a.y, a.status);
 }
 
 }  // namespace e2ttt

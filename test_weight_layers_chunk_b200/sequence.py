@@ -398,14 +398,17 @@ def ssm_step(q, k, v, dt, S, A, D=None, *, out=None, stream=None):
 
 # ---------------------------------------------------------------- gradient norm
 def _grad_lists(tensors, name):
-    """Pointers, counts and types of contiguous CUDA tensors on one device."""
-    dev = tensors[0].device
-    for i, t in enumerate(tensors):
-        if t.dtype not in _ACT or not t.is_cuda or t.device != dev or not t.is_contiguous():
-            _refuse(f"{name}[{i}] must be a contiguous bfloat16 or float32 tensor on one CUDA device, "
-                    f"got {t.dtype} on {t.device}")
-    return ([t.data_ptr() for t in tensors], [t.numel() for t in tensors],
-            [_ACT[t.dtype] for t in tensors], dev)
+    """Pointers, counts, types and device of contiguous CUDA tensors on one device."""
+    T = torch.Tensor
+    try:
+        act = [_ACT[t.dtype] for t in tensors]
+        devs = set(map(T.get_device, tensors))
+        fine = len(devs) == 1 and -1 not in devs and all(map(T.is_contiguous, tensors))
+    except (KeyError, AttributeError, TypeError):
+        fine = False
+    if not fine:
+        _refuse(f"{name} must be contiguous bfloat16 or float32 tensors on one CUDA device")
+    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), act, tensors[0].device
 
 
 def grad_norm(grads, *, ws=None, stream=None):

@@ -251,172 +251,342 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
+// ------------------------------------------------------------------ two streams of heads
+// The chunk-state and output kernels take one chunk of one group and a run of
+// its items (a head, and a tile of 64 state rows where there are several). The
+// tile that all heads share is loaded once; two groups of 128 threads then take
+// the items in turn, each with its own buffers, accumulators and barriers, so
+// that one group's MMAs and loads run under the other's arithmetic.
+constexpr int kHalf = kThreads / 2;
+
+__device__ __forceinline__ void group_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory"); }
+// Whether `ok` holds for all of the group's threads.
+__device__ __forceinline__ bool group_and(int wg, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(wg + 1), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+// Shared-memory writes of the group become visible to the MMAs; the group meets.
+__device__ __forceinline__ void group_publish(int wg) {
+  tc::fence_async_smem();
+  tc::tc_fence_before();
+  group_sync(wg);
+  tc::tc_fence_after();
+}
+// Mmas::wait() for a group of 128 threads with an mbarrier of its own.
+struct GroupMmas {
+  uint64_t* bar;
+  uint32_t phase;
+  int* status;
+  int wg;
+  __device__ __forceinline__ bool wait() {
+    const bool ok = tc::mbar_wait(bar, phase);
+    if (!ok) atomicExch(status, tc2::kErrMma);
+    const bool all = group_and(wg, ok);
+    if (!all) (void)tc::mbar_wait(bar, phase);
+    phase ^= 1u;
+    tc::tc_fence_after();
+    return all;
+  }
+};
+
+// Rows of one item by the 128 threads of a group (cp.async where VEC).
+template <int ROWS, int BLOCKS, bool VEC>
+__device__ __forceinline__ void group_load_rows(uint8_t* tile, const bf16* src, long long ld, int n, int cols) {
+  constexpr int kPer = BLOCKS * 8, kStep = kHalf / kPer;
+  static_assert(kStep % 8 == 0 && ROWS % kStep == 0, "a thread's rows share their swizzle");
+  const int tid = threadIdx.x % kHalf, j = tid % kPer, r0 = tid / kPer;
+  const int left = j * 8 < cols ? n - r0 : 0;
+  const bf16* p = src + r0 * ld + j * 8;
+  uint8_t* dst = tile + piece<ROWS>(r0, j);
+#pragma unroll
+  for (int i = 0; i < ROWS / kStep; ++i) {
+    const bool on = i * kStep < left;
+    if constexpr (VEC)
+      cp16(smem_u32(dst) + i * kStep * 128, on ? p : src, on);
+    else
+      *reinterpret_cast<uint4*>(dst + i * kStep * 128) =
+          on ? load8(src + (long long)(r0 + i * kStep) * ld, j * 8, cols) : uint4{0, 0, 0, 0};
+    p += kStep * ld;
+  }
+}
+
+struct Items {
+  int b, g, c, t0, n, i0, i1, HG;
+};
+__device__ __forceinline__ Items block_items(const SsmDims& s, const int* lengths, int per) {
+  Items m;
+  m.c = blockIdx.x;
+  m.b = blockIdx.y / s.G;
+  m.g = blockIdx.y - m.b * s.G;
+  m.HG = s.H / s.G;
+  m.t0 = m.c * kQ;
+  m.n = min(max(ssm_row_length(lengths, m.b, s.T) - m.t0, 0), kQ);
+  m.i0 = blockIdx.z * per;
+  m.i1 = min(m.HG * s.NPT, m.i0 + per);
+  return m;
+}
+
 // ------------------------------------------------------------------ chunk states
 // states[c][bh][p][n] = sum_s w_s x_s[p] y_s[n]: with REV 0 x = v, y = k,
 // w_s = e^{c_Q-c_s} eta_s; with REV 1 x = dy, y = q, w_t = e^{c_t}. D[n][p] on
-// the tensor cores (128 state columns as rows of the tile): y contracted over
-// its rows, w x in three terms.
+// the tensor cores: y contracted over its rows (128 state columns as rows of the
+// tile), against the three terms of w x side by side, so that y is read once for
+// all three (N = 192: 80 cycles of shared-memory reads a step instead of 144).
 template <int REV, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     state_kernel(SsmDims s, const bf16* __restrict__ x, const bf16* __restrict__ y,
                  const float* __restrict__ logs, const int* __restrict__ lengths,
-                 float* __restrict__ states, int* __restrict__ status) {
+                 float* __restrict__ states, int per, int* __restrict__ status) {
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(16) float slog[3 * kQ];
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, gbar[2];
   __shared__ uint32_t slot;
-  uint8_t* ys = align1k(raw);   // [kQ][128]
-  uint8_t* xs = ys + kQ * 256;  // three of [kQ][64]
-  const int bh = blockIdx.y, b = bh / s.H, h = bh - b * s.H, g = h / (s.H / s.G);
-  const int c = blockIdx.x, t0 = c * kQ, p0 = blockIdx.z * kPT, np = min(kPT, s.P - p0);
-  const ChunkLogs L = logs_view(slog);
-  const uint32_t tmem = block_begin<64>(&bar, &slot);
+  uint8_t* ys = align1k(raw);  // [kQ][128]
+  const int wg = threadIdx.x / kHalf, t = threadIdx.x % kHalf, quad = t >> 5;
+  uint8_t* xs = ys + kQ * 256 + wg * 3 * kQ * 128;  // three of [kQ][64]
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&gbar[0], 1);
+    tc::mbar_init(&gbar[1], 1);
+  }
+  const uint32_t tmem = block_begin<512>(&bar, &slot) + wg * 192;
   griddep_wait();
   griddep_launch_dependents();
-  const int n = min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ);
-  load_rows<kQ, 2, VEC>(ys, y + (((long long)b * s.G + g) * s.T + t0) * s.N, s.N, n, s.N);
-  load_logs(L, logs, bh, s.NC, c);
-  const int r = threadIdx.x >> 1, j0 = (threadIdx.x & 1) * 4;
-  const bf16* xr = x + ((long long)bh * s.T + t0 + r) * s.P + p0;
-  uint4 xv[4];
+  const Items m = block_items(s, lengths, per);
+  load_rows<kQ, 2, VEC>(ys, y + (((long long)m.b * s.G + m.g) * s.T + m.t0) * s.N, s.N, m.n, s.N);
+  uint4 xv[8];
+  float hi = 0.f, lo = 0.f, eta = 0.f, end_hi = 0.f, end_lo = 0.f;
+  // This thread's row of the item, and its token's logs.
+  auto fetch = [&](int it) {
+    const int h = m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT, bh = m.b * s.H + h;
+    const int np = min(kPT, s.P - p0);
+    const bf16* xr = x + ((long long)bh * s.T + m.t0 + t) * s.P + p0;
+    const float* lg = logs + ((long long)bh * s.NC + m.c) * 3 * kQ;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int col = (j0 + j) * 8;
-    xv[j] = uint4{0, 0, 0, 0};
-    if (r < n && col < np) xv[j] = VEC ? *reinterpret_cast<const uint4*>(xr + col) : load8(xr, col, np);
-  }
-  __syncthreads();
-  const float w = REV ? L.from_start(r) : L.to_end(r) * L.eta[r];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t* u = &xv[j].x;
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = w * lo_f(u[i]);
-      f[2 * i + 1] = w * hi_f(u[i]);
+    for (int j = 0; j < 8; ++j) {
+      xv[j] = uint4{0, 0, 0, 0};
+      if (t < m.n && j * 8 < np) xv[j] = VEC ? *reinterpret_cast<const uint4*>(xr + j * 8) : load8(xr, j * 8, np);
     }
-    uint4 t[3];
-    split3(f, t);
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      *reinterpret_cast<uint4*>(xs + i * kQ * 128 + piece<kQ>(r, j0 + j)) = t[i];
-  }
+    hi = lg[t];
+    lo = lg[kQ + t];
+    if (!REV) {
+      eta = lg[2 * kQ + t];
+      end_hi = lg[kQ - 1];
+      end_lo = lg[2 * kQ - 1];
+    }
+  };
+  int it = m.i0 + wg;
+  if (it < m.i1) fetch(it);
   cp_wait();
   publish();
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) mma<kQ, true, kQ, true, 64>(tmem, ys, xs + i * kQ * 128, kQ / 16, i > 0);
-    tc::mma_commit(&bar);
-  }
-  Mmas done{&bar, 0u, status};
-  if (done.wait()) {
-    const int warp = threadIdx.x >> 5, quad = warp & 3, half = warp >> 2;
-    const int nn = quad * 32 + (threadIdx.x & 31);
-    float v[32];
-    tc::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + half * 32, v);
-    float* out = states + (((long long)c * s.B * s.H + bh) * s.P + p0 + half * 32) * s.N + nn;
-    if (nn < s.N)
+  GroupMmas done{&gbar[wg], 0u, status, wg};
+#pragma unroll 1
+  for (; it < m.i1; it += 2) {
+    const float w = REV ? ex2(hi + lo) : ex2((end_hi - hi) + (end_lo - lo)) * eta;
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (half * 32 + j < np) out[(long long)j * s.N] = v[j];
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t* u = &xv[j].x;
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = w * lo_f(u[i]);
+        f[2 * i + 1] = w * hi_f(u[i]);
+      }
+      uint4 term[3];
+      split3(f, term);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(xs + i * kQ * 128 + piece<kQ>(t, j)) = term[i];
+    }
+    group_publish(wg);
+    if (t == 0) {
+      mma<kQ, true, kQ, true, 192>(tmem, ys, xs, kQ / 16, false);
+      tc::mma_commit(&gbar[wg]);
+    }
+    if (it + 2 < m.i1) fetch(it + 2);
+    if (!done.wait()) break;
+    const int h = m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT, bh = m.b * s.H + h;
+    const int np = min(kPT, s.P - p0);
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    float* out = states + (((long long)m.c * s.B * s.H + bh) * s.P + p0) * s.N + t;
+    if (quad * 32 < s.N) {
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        float a0[32], a1[32], a2[32];
+        tc::tmem_ld32(lanes + half * 32, a0);
+        tc::tmem_ld32(lanes + 64 + half * 32, a1);
+        tc::tmem_ld32(lanes + 128 + half * 32, a2);
+        if (t < s.N)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (half * 32 + j < np) *out = a0[j] + (a1[j] + a2[j]);
+            out += s.N;
+          }
+      }
+    }
+    tc::tc_fence_before();
+    group_sync(wg);  // the accumulators are read before the next item's MMAs write them
+    tc::tc_fence_after();
   }
-  block_end<64>(tmem);
+  block_end<512>(tmem - wg * 192);
 }
 
 // ------------------------------------------------------------------ outputs
-// The decay between token t (this thread's row) and the columns of a 32-token
-// block: exactly within the row's own block, and as e^{c_t - c_r} e^{c_r - c_s}
-// with r the last token of an earlier block (two factors that are both at most
-// one for a decaying state), so that only a quarter of them takes an exponential
-// each. `tail[s]` holds e^{c_r - c_s} (times eta_s where asked).
-__device__ __forceinline__ void fill_tails(const ChunkLogs& L, float* tail, bool with_eta) {
-  if (threadIdx.x < kQ)
-    tail[threadIdx.x] = L.decay(threadIdx.x | 31, threadIdx.x) * (with_eta ? L.eta[threadIdx.x] : 1.f);
-}
-
+// The scores q k^T are the same for all heads of a group: they are made once and
+// stay in tensor memory. An item turns them into its decayed scores W,
+//   W_ts = e^{c_t-c_s} eta_s q_t.k_s, s <= t
+// the decay taken exactly within the row's own block of 32 tokens, and as
+// e^{c_t-c_r} e^{c_r-c_s} with r the last token of an earlier block (two factors
+// that are both at most one for a decaying state), so that only a quarter of the
+// decays takes an exponential each.
 template <int NB, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     out_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,
                const bf16* __restrict__ v, const float* __restrict__ logs,
                const float* __restrict__ D, const int* __restrict__ lengths,
-               const bf16* __restrict__ states, bf16* __restrict__ y, int* __restrict__ status) {
+               const bf16* __restrict__ states, bf16* __restrict__ y, int per,
+               int* __restrict__ status) {
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(16) float slog[3 * kQ];
-  __shared__ float tail[kQ];
-  __shared__ uint64_t bar;
+  __shared__ __align__(16) float slog[2][3 * kQ], stail[2][kQ];
+  __shared__ uint64_t bar, gbar[2];
   __shared__ uint32_t slot;
-  uint8_t* qs = align1k(raw);          // [kQ][NB * 64]
-  uint8_t* vs = qs + NB * kQ * 128;    // [kQ][64]
-  uint8_t* Ss = vs + kQ * 128;         // [64][NB * 64]
-  uint8_t* ks = Ss + NB * kPT * 128;   // [kQ][NB * 64], then the scores [kQ][kQ]
-  const int bh = blockIdx.y, b = bh / s.H, h = bh - b * s.H, g = h / (s.H / s.G);
-  const int c = blockIdx.x, t0 = c * kQ, p0 = blockIdx.z * kPT, np = min(kPT, s.P - p0);
-  const ChunkLogs L = logs_view(slog);
-  const uint32_t tmem = block_begin<256>(&bar, &slot);
+  const int wg = threadIdx.x / kHalf, t = threadIdx.x % kHalf, quad = t >> 5;
+  uint8_t* qs = align1k(raw);               // [kQ][NB * 64]
+  uint8_t* ks = qs + NB * kQ * 128;         // [kQ][NB * 64], then group 0's scores
+  uint8_t* Ws = ks + wg * kQ * 256;         // [kQ][kQ]
+  uint8_t* Ss = ks + 2 * kQ * 256 + wg * NB * kPT * 128;                        // [64][NB * 64]
+  uint8_t* vs = ks + 2 * kQ * 256 + 2 * NB * kPT * 128 + wg * 2 * kQ * 128;     // two of [kQ][64]
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&gbar[0], 1);
+    tc::mbar_init(&gbar[1], 1);
+  }
+  const uint32_t tmem = block_begin<512>(&bar, &slot);
   griddep_wait();
   griddep_launch_dependents();
-  const int n = min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ);
-  const long long qo = (((long long)b * s.G + g) * s.T + t0) * s.N;
-  load_rows<kQ, NB, VEC>(qs, q + qo, s.N, n, s.N);
-  load_rows<kQ, NB, VEC>(ks, k + qo, s.N, n, s.N);
-  load_rows<kPT, NB, VEC>(Ss, states + (((long long)c * s.B * s.H + bh) * s.P + p0) * s.N, s.N, np, s.N);
-  load_rows<kQ, 1, VEC>(vs, v + ((long long)bh * s.T + t0) * s.P + p0, s.P, n, np);
-  load_logs(L, logs, bh, s.NC, c);
+  const Items m = block_items(s, lengths, per);
+  const long long qo = (((long long)m.b * s.G + m.g) * s.T + m.t0) * s.N;
+  load_rows<kQ, NB, VEC>(qs, q + qo, s.N, m.n, s.N);
+  load_rows<kQ, NB, VEC>(ks, k + qo, s.N, m.n, s.N);
+  float hi = 0.f, lo = 0.f, eta = 0.f;
+  auto fetch_logs = [&](int it) {
+    const float* lg = logs + ((long long)(m.b * s.H + m.g * m.HG + it / s.NPT) * s.NC + m.c) * 3 * kQ;
+    hi = lg[t];
+    lo = lg[kQ + t];
+    eta = lg[2 * kQ + t];
+  };
+  auto fetch_state = [&](int it) {
+    const int bh = m.b * s.H + m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT;
+    group_load_rows<kPT, NB, VEC>(Ss, states + (((long long)m.c * s.B * s.H + bh) * s.P + p0) * s.N, s.N,
+                                  min(kPT, s.P - p0), s.N);
+  };
+  auto fetch_rows = [&](int it, int buf) {
+    const int bh = m.b * s.H + m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT;
+    group_load_rows<kQ, 1, VEC>(vs + buf * kQ * 128, v + ((long long)bh * s.T + m.t0) * s.P + p0, s.P, m.n,
+                                min(kPT, s.P - p0));
+  };
+  int it = m.i0 + wg;
+  if (it < m.i1) {
+    fetch_logs(it);
+    fetch_state(it);
+    fetch_rows(it, 0);
+  }
   cp_wait();
   publish();
   const int nsteps = (s.N + 15) / 16;
-  constexpr uint32_t kM = 0, kYi = 128, kYd = 192;
-  Mmas done{&bar, 0u, status};
+  Mmas first{&bar, 0u, status};
   if (threadIdx.x == 0) {
-    mma<kQ, false, kQ, false, 128>(tmem + kM, qs, ks, nsteps, false);
-    mma<kQ, false, kPT, false, 64>(tmem + kYi, qs, Ss, nsteps, false);
+    mma<kQ, false, kQ, false, 128>(tmem, qs, ks, nsteps, false);
     tc::mma_commit(&bar);
   }
-  fill_tails(L, tail, true);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = warp >> 2;
-  const int t = quad * 32 + lane;
+  const uint32_t kYi = 128 + wg * 128, kYd = kYi + 64;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-  if (done.wait()) {
-#pragma unroll 1
-    for (int cb = half; cb < 4; cb += 2) {
-      uint4 o[4];
-      uint32_t* ow = &o[0].x;
-      if (cb <= quad) {
-        float m[32];
-        tc::tmem_ld32(lanes + kM + cb * 32, m);
-        const float row = cb < quad ? L.decay(t, cb * 32 + 31) : 0.f;
+  if (first.wait()) {
+    // the scores above the diagonal blocks are zero for every item
+    for (int cb = quad + 1; cb < 4; ++cb)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int u = cb * 32 + i;
-          if (cb < quad)
-            m[i] *= row * tail[u];
-          else
-            m[i] = u <= t ? m[i] * (L.decay(t, u) * L.eta[u]) : 0.f;
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, cb * 4 + i)) = uint4{0, 0, 0, 0};
+    GroupMmas done{&gbar[wg], 0u, status, wg};
+    const ChunkLogs L = logs_view(slog[wg]);
+    float* tail = stail[wg];
+    int buf = 0;
+#pragma unroll 1
+    for (; it < m.i1; it += 2, buf ^= 1) {
+      const int h = m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT, bh = m.b * s.H + h;
+      const int np = min(kPT, s.P - p0);
+      L.hi[t] = hi;
+      L.lo[t] = lo;
+      L.eta[t] = eta;
+      tail[t] = ex2((__shfl_sync(~0u, hi, 31) - hi) + (__shfl_sync(~0u, lo, 31) - lo)) * eta;
+      const float f = ex2(hi + lo), thi = hi, tlo = lo;
+      cp_wait();
+      group_publish(wg);  // the item's rows, state and logs are there
+      if (t == 0) {
+        mma<kQ, false, kPT, false, 64>(tmem + kYi, qs, Ss, nsteps, false);
+        tc::mma_commit(&gbar[wg]);
+      }
+      if (it + 2 < m.i1) {
+        fetch_logs(it + 2);
+        fetch_rows(it + 2, buf ^ 1);
+      }
+#pragma unroll 1
+      for (int cb = 0; cb < quad; ++cb) {
+        float a[32];
+        tc::tmem_ld32(lanes + cb * 32, a);
+        const float row = ex2((thi - L.hi[cb * 32 + 31]) + (tlo - L.lo[cb * 32 + 31]));
+        uint4 o[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 w = *reinterpret_cast<const float4*>(tail + cb * 32 + i * 4);
+          uint32_t* ow = &o[i >> 1].x + (i & 1) * 2;
+          ow[0] = pack2(a[i * 4] * (row * w.x), a[i * 4 + 1] * (row * w.y));
+          ow[1] = pack2(a[i * 4 + 2] * (row * w.z), a[i * 4 + 3] * (row * w.w));
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ow[i] = pack2(m[2 * i], m[2 * i + 1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = uint4{0, 0, 0, 0};
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, cb * 4 + i)) = o[i];
       }
+      {
+        float a[32];
+        tc::tmem_ld32(lanes + quad * 32, a);
+        uint4 o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(ks + piece<kQ>(t, cb * 4 + i)) = o[i];
-    }
-    publish();
-    if (threadIdx.x == 0) {
-      mma<kQ, false, kQ, true, 64>(tmem + kYd, ks, vs, kQ / 16, false);
-      tc::mma_commit(&bar);
-    }
-    if (done.wait()) {
-      float yi[32], yd[32];
-      tc::tmem_ld32(lanes + kYi + half * 32, yi);
-      tc::tmem_ld32(lanes + kYd + half * 32, yd);
-      const float f = L.from_start(t), Dh = D ? D[h] : 0.f;
-      bf16* out = y + ((long long)bh * s.T + t0 + t) * s.P + p0 + half * 32;
-      if (t0 + t < s.T)
+        for (int i = 0; i < 8; ++i) {
+          const int u = quad * 32 + i * 4, d = t - u;
+          const float4 uh = *reinterpret_cast<const float4*>(L.hi + u);
+          const float4 ul = *reinterpret_cast<const float4*>(L.lo + u);
+          const float4 ue = *reinterpret_cast<const float4*>(L.eta + u);
+          const float w0 = d >= 0 ? a[i * 4] * (ex2((thi - uh.x) + (tlo - ul.x)) * ue.x) : 0.f;
+          const float w1 = d >= 1 ? a[i * 4 + 1] * (ex2((thi - uh.y) + (tlo - ul.y)) * ue.y) : 0.f;
+          const float w2 = d >= 2 ? a[i * 4 + 2] * (ex2((thi - uh.z) + (tlo - ul.z)) * ue.z) : 0.f;
+          const float w3 = d >= 3 ? a[i * 4 + 3] * (ex2((thi - uh.w) + (tlo - ul.w)) * ue.w) : 0.f;
+          uint32_t* ow = &o[i >> 1].x + (i & 1) * 2;
+          ow[0] = pack2(w0, w1);
+          ow[1] = pack2(w2, w3);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, quad * 4 + i)) = o[i];
+      }
+      group_publish(wg);
+      uint8_t* vb = vs + buf * kQ * 128;
+      if (t == 0) mma<kQ, false, kQ, true, 64>(tmem + kYd, Ws, vb, kQ / 16, false);
+      if (!done.wait()) break;  // of the state's product: its tile is free
+      if (t == 0) tc::mma_commit(&gbar[wg]);
+      if (it + 2 < m.i1) fetch_state(it + 2);
+      if (!done.wait()) break;
+      const float Dh = D ? D[h] : 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float yi[32], yd[32];
+        tc::tmem_ld32(lanes + kYi + half * 32, yi);
+        tc::tmem_ld32(lanes + kYd + half * 32, yd);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(vs + piece<kQ>(t, half * 4 + i));
+          uint4* at = reinterpret_cast<uint4*>(vb + piece<kQ>(t, half * 4 + i));
+          const uint4 xv = *at;
           const uint32_t* xu = &xv.x;
           uint4 o;
           uint32_t* ou = &o.x;
@@ -425,13 +595,33 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int a = i * 8 + e * 2;
             const float y0 = fmaf(f, yi[a], yd[a]) + Dh * lo_f(xu[e]);
             const float y1 = fmaf(f, yi[a + 1], yd[a + 1]) + Dh * hi_f(xu[e]);
-            ou[e] = t < n ? pack2(y0, y1) : 0u;
+            ou[e] = t < m.n ? pack2(y0, y1) : 0u;
           }
-          store8<VEC>(out + i * 8, o, np - (half * 32 + i * 8));
+          *at = o;  // y takes the place of v
         }
+      }
+      tc::tc_fence_before();
+      group_sync(wg);
+      tc::tc_fence_after();
+      // whole rows to memory: eight threads a row
+      bf16* out = y + ((long long)bh * s.T + m.t0) * s.P + p0;
+      const int j = t & 7;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = (t >> 3) + i * 16;
+        if (m.t0 + r < s.T)
+          store8<VEC>(out + (long long)r * s.P + j * 8, *reinterpret_cast<const uint4*>(vb + piece<kQ>(r, j)),
+                      np - j * 8);
+      }
     }
   }
-  block_end<256>(tmem);
+  block_end<512>(tmem);
+}
+
+// The decays' second factors, for the gradients: e^{c_r - c_s} with r the last
+// token of s's block of 32.
+__device__ __forceinline__ void fill_tails(const ChunkLogs& L, float* tail) {
+  if (threadIdx.x < kQ) tail[threadIdx.x] = L.decay(threadIdx.x | 31, threadIdx.x);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -600,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, x2, kPT / 16, true);
       tc::mma_commit(&bar);
     }
-    fill_tails(L, tail, false);
+    fill_tails(L, tail);
     if (!(ok = done.wait())) break;
     // the states' parts of dq and dk, and their dots with q and k
     {
@@ -820,10 +1010,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   block_end<512>(tmem);
 }
 
-size_t state_smem() { return 1024 + kQ * 256 + 3 * kQ * 128; }
+size_t state_smem() { return 1024 + kQ * 256 + 2 * 3 * kQ * 128; }
 template <int NB>
 size_t out_smem() {
-  return 1024 + NB * kQ * 128 + kQ * 128 + NB * kPT * 128 + kQ * 256;
+  return 1024 + NB * kQ * 128 + 2 * kQ * 256 + 2 * NB * kPT * 128 + 4 * kQ * 128;
 }
 
 template <int NB>
@@ -831,10 +1021,10 @@ size_t grad_smem() {
   return 1024 + 2 * NB * kQ * 128 + 2 * kQ * 128 + 2 * kQ * 256 + (NB == 1 ? 1 : 2) * NB * kPT * 128;
 }
 
-// How many blocks share the heads of a group (and their state tiles) in the
-// gradients. A block's fixed part (q, k, the results) weighs about a third of an
-// item; every part more is one more fp32 copy of dq and dk to write and add up.
-int grad_parts(const SsmDims& s) {
+// How many blocks share the items of a group's chunk: of all ways, the one whose
+// waves of blocks, each of `fixed` + its longest stream of items, end first. `part`
+// is what one block more adds in memory traffic. All in units of an item's time.
+int item_parts(const SsmDims& s, int streams, double fixed, double part) {
   constexpr int kSms = 148;
   const long long items = (long long)s.H / s.G * s.NPT, base = (long long)s.B * s.G * s.NC;
   int best = 1;
@@ -842,10 +1032,20 @@ int grad_parts(const SsmDims& s) {
   for (long long ns = 1; ns <= items; ++ns) {
     const long long per = (items + ns - 1) / ns;
     if ((items + per - 1) / per != ns) continue;
-    const double c = (double)((base * ns + kSms - 1) / kSms) * (per + 0.35) + 0.04 * ns * base / kSms;
+    const double c = (double)((base * ns + kSms - 1) / kSms) * ((per + streams - 1) / streams + fixed) +
+                     part * ns * base / kSms;
     if (c < cost) cost = c, best = (int)ns;
   }
   return best;
+}
+// The gradients: q, k and the results weigh about a third of an item; every part
+// more is one more fp32 copy of dq and dk to write and add up.
+int grad_parts(const SsmDims& s) { return item_parts(s, 1, 0.35, 0.04); }
+
+dim3 item_grid(const SsmDims& s, int parts, int* per) {
+  const long long items = (long long)s.H / s.G * s.NPT;
+  *per = (int)((items + parts - 1) / parts);
+  return dim3(s.NC, s.B * s.G, parts);
 }
 
 template <class F>
@@ -871,8 +1071,7 @@ int ssm_tc_grad_parts(const SsmDims& s) { return grad_parts(s); }
 cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
   const SsmDims& s = a.s;
   const int BH = s.B * s.H, parts = grad_parts(s);
-  const long long items = (long long)s.H / s.G * s.NPT;
-  const int per = (int)((items + parts - 1) / parts);
+  int per = 0;
   const bool vec = vectors(s, {a.q, a.k, a.v, a.dy, a.dq, a.dk, a.dv, a.states});
   cudaError_t e;
   {
@@ -885,8 +1084,9 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
     E2TTT_TRACE("ssm_chunk_dstate", a.st);
     auto kern = vec ? state_kernel<1, true> : state_kernel<1, false>;
     if ((e = allow_smem(kern, state_smem())) != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(s.NC, BH, s.NPT), dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.dy,
-                   (const bf16*)a.q, (const float*)w.logs, a.lengths, w.ends, w.status);
+    const dim3 grid = item_grid(s, item_parts(s, 2, 1.5, 0), &per);
+    e = launch_pdl(kern, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.dy, (const bf16*)a.q,
+                   (const float*)w.logs, a.lengths, w.ends, per, w.status);
     if (e != cudaSuccess) return e;
   }
   if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, nullptr, true, a.st)) != cudaSuccess) return e;
@@ -897,7 +1097,8 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
     const size_t smem = s.N <= 64 ? grad_smem<1>() : grad_smem<2>();
     if ((e = allow_smem(kern, smem)) != cudaSuccess) return e;
     const GradOut o{w.dq, w.dk, (bf16*)a.dq, (bf16*)a.dk, (bf16*)a.dv, w.ddt, w.dA, w.dD};
-    e = launch_pdl(kern, dim3(s.NC, s.B * s.G, parts), dim3(kThreads), smem, a.st, s, (const bf16*)a.q,
+    const dim3 grid = item_grid(s, parts, &per);
+    e = launch_pdl(kern, grid, dim3(kThreads), smem, a.st, s, (const bf16*)a.q,
                    (const bf16*)a.k, (const bf16*)a.v, (const bf16*)a.dy, (const float*)w.logs, a.A, a.D, a.lengths,
                    a.states, (const float*)w.ends, o, per, w.status);
     if (e != cudaSuccess) return e;
@@ -908,7 +1109,8 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
 cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
   const SsmDims& s = a.s;
   const int BH = s.B * s.H;
-  const dim3 grid(s.NC, BH, s.NPT);
+  int per = 0;
+  const dim3 grid = item_grid(s, item_parts(s, 2, 1.5, 0), &per);
   const bool vec = vectors(s, {a.q, a.k, a.v, a.y});
   cudaError_t e;
   {
@@ -922,7 +1124,7 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
     auto kern = vec ? state_kernel<0, true> : state_kernel<0, false>;
     if ((e = allow_smem(kern, state_smem())) != cudaSuccess) return e;
     e = launch_pdl(kern, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.v, (const bf16*)a.k,
-                   (const float*)a.logs, a.lengths, a.states, a.status);
+                   (const float*)a.logs, a.lengths, a.states, per, a.status);
     if (e != cudaSuccess) return e;
   }
   if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, a.starts, a.keep, a.st)) != cudaSuccess) return e;
@@ -933,7 +1135,7 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
   if ((e = allow_smem(kern, smem)) != cudaSuccess) return e;
   return launch_pdl(kern, grid, dim3(kThreads), smem, a.st, s, (const bf16*)a.q, (const bf16*)a.k,
                     (const bf16*)a.v, (const float*)a.logs, a.D, a.lengths, (const bf16*)a.starts,
-                    (bf16*)a.y, a.status);
+                    (bf16*)a.y, per, a.status);
 }
 
 }  // namespace e2ttt

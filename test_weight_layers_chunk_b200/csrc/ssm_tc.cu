@@ -25,7 +25,7 @@ using tc2::idesc;
 using tc2::smem_u32;
 
 constexpr int kQ = kSsmTcChunk;  // tokens per chunk
-constexpr int kThreads = 256;    // 8 warps: tensor-memory lanes 32 (w & 3), column half w >> 2
+constexpr int kThreads = 512;    // 16 warps: tensor-memory lanes 32 (w & 3), a share of the columns each
 constexpr int kPT = kSsmPT;
 
 // Byte offset of 16-byte piece `j` (8 columns) of row r in a tile of ROWS rows.
@@ -151,9 +151,6 @@ __device__ __forceinline__ void load8f(float (&f)[8], const float* p, int left) 
     for (int e = 0; e < 8; ++e) f[e] = e < left ? p[e] : 0.f;
   }
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
 
 // f as three bf16 terms: f = t0 + t1 + t2 to 24 bits.
 __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
@@ -247,6 +244,41 @@ __device__ __forceinline__ void publish() {
   tc::tc_fence_after();
 }
 
+// 16 columns of this thread's lane from each of N places.
+template <int N>
+__device__ __forceinline__ void tmem_ld16(const uint32_t (&at)[N], float (&x)[N][16]) {
+  uint32_t r[N][16];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[n][0]), "=r"(r[n][1]), "=r"(r[n][2]), "=r"(r[n][3]), "=r"(r[n][4]), "=r"(r[n][5]),
+          "=r"(r[n][6]), "=r"(r[n][7]), "=r"(r[n][8]), "=r"(r[n][9]), "=r"(r[n][10]), "=r"(r[n][11]),
+          "=r"(r[n][12]), "=r"(r[n][13]), "=r"(r[n][14]), "=r"(r[n][15])
+        : "r"(at[n])
+        : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      asm volatile("" : "+r"(r[n][i]));  // no use of it moves before the wait
+      x[n][i] = __uint_as_float(r[n][i]);
+    }
+}
+
+// 16 columns of this thread's lane, to tensor memory (complete on return).
+__device__ __forceinline__ void tmem_st16(uint32_t at, const float (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(x[8]),
+      "f"(x[9]), "f"(x[10]), "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), "f"(x[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
@@ -254,19 +286,20 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
 // ------------------------------------------------------------------ two streams of heads
 // The chunk-state and output kernels take one chunk of one group and a run of
 // its items (a head, and a tile of 64 state rows where there are several). The
-// tile that all heads share is loaded once; two groups of 128 threads then take
+// tile that all heads share is loaded once; two groups of 256 threads then take
 // the items in turn, each with its own buffers, accumulators and barriers, so
-// that one group's MMAs and loads run under the other's arithmetic.
+// that one group's MMAs and loads run under the other's arithmetic. A row (token)
+// has two threads, one for each half of its columns.
 constexpr int kHalf = kThreads / 2;
 
-__device__ __forceinline__ void group_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory"); }
+__device__ __forceinline__ void group_sync(int wg) { asm volatile("bar.sync %0, 256;" ::"r"(wg + 1) : "memory"); }
 // Whether `ok` holds for all of the group's threads.
 __device__ __forceinline__ bool group_and(int wg, bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.and.pred q, %1, 128, p;\n\t"
+      "barrier.cta.red.and.pred q, %1, 256, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
       : "r"(wg + 1), "r"((uint32_t)ok)
@@ -280,7 +313,7 @@ __device__ __forceinline__ void group_publish(int wg) {
   group_sync(wg);
   tc::tc_fence_after();
 }
-// Mmas::wait() for a group of 128 threads with an mbarrier of its own.
+// Mmas::wait() for a group of 256 threads with an mbarrier of its own.
 struct GroupMmas {
   uint64_t* bar;
   uint32_t phase;
@@ -297,7 +330,7 @@ struct GroupMmas {
   }
 };
 
-// Rows of one item by the 128 threads of a group (cp.async where VEC).
+// Rows of one item by the threads of a group (cp.async where VEC).
 template <int ROWS, int BLOCKS, bool VEC>
 __device__ __forceinline__ void group_load_rows(uint8_t* tile, const bf16* src, long long ld, int n, int cols) {
   constexpr int kPer = BLOCKS * 8, kStep = kHalf / kPer;
@@ -349,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t bar, gbar[2];
   __shared__ uint32_t slot;
   uint8_t* ys = align1k(raw);  // [kQ][128]
-  const int wg = threadIdx.x / kHalf, t = threadIdx.x % kHalf, quad = t >> 5;
+  const int wg = threadIdx.x / kHalf, t = threadIdx.x % kQ, half = threadIdx.x / kQ & 1, quad = t >> 5;
   uint8_t* xs = ys + kQ * 256 + wg * 3 * kQ * 128;  // three of [kQ][64]
   if (threadIdx.x == 0) {
     tc::mbar_init(&gbar[0], 1);
@@ -360,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   const Items m = block_items(s, lengths, per);
   load_rows<kQ, 2, VEC>(ys, y + (((long long)m.b * s.G + m.g) * s.T + m.t0) * s.N, s.N, m.n, s.N);
-  uint4 xv[8];
+  uint4 xv[4];
   float hi = 0.f, lo = 0.f, eta = 0.f, end_hi = 0.f, end_lo = 0.f;
   // This thread's row of the item, and its token's logs.
   auto fetch = [&](int it) {
@@ -369,9 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bf16* xr = x + ((long long)bh * s.T + m.t0 + t) * s.P + p0;
     const float* lg = logs + ((long long)bh * s.NC + m.c) * 3 * kQ;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
+      const int col = half * 32 + j * 8;
       xv[j] = uint4{0, 0, 0, 0};
-      if (t < m.n && j * 8 < np) xv[j] = VEC ? *reinterpret_cast<const uint4*>(xr + j * 8) : load8(xr, j * 8, np);
+      if (t < m.n && col < np) xv[j] = VEC ? *reinterpret_cast<const uint4*>(xr + col) : load8(xr, col, np);
     }
     hi = lg[t];
     lo = lg[kQ + t];
@@ -390,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (; it < m.i1; it += 2) {
     const float w = REV ? ex2(hi + lo) : ex2((end_hi - hi) + (end_lo - lo)) * eta;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const uint32_t* u = &xv[j].x;
       float f[8];
 #pragma unroll
@@ -401,10 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4 term[3];
       split3(f, term);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(xs + i * kQ * 128 + piece<kQ>(t, j)) = term[i];
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(xs + i * kQ * 128 + piece<kQ>(t, half * 4 + j)) = term[i];
     }
     group_publish(wg);
-    if (t == 0) {
+    if (threadIdx.x % kHalf == 0) {
       mma<kQ, true, kQ, true, 192>(tmem, ys, xs, kQ / 16, false);
       tc::mma_commit(&gbar[wg]);
     }
@@ -413,20 +447,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT, bh = m.b * s.H + h;
     const int np = min(kPT, s.P - p0);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    float* out = states + (((long long)m.c * s.B * s.H + bh) * s.P + p0) * s.N + t;
+    float* out = states + (((long long)m.c * s.B * s.H + bh) * s.P + p0 + half * 32) * s.N + t;
     if (quad * 32 < s.N) {
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        float a0[32], a1[32], a2[32];
-        tc::tmem_ld32(lanes + half * 32, a0);
-        tc::tmem_ld32(lanes + 64 + half * 32, a1);
-        tc::tmem_ld32(lanes + 128 + half * 32, a2);
-        if (t < s.N)
+      for (int cb = half * 32; cb < half * 32 + 32; cb += 16) {
+        float ld[3][16];
+        tmem_ld16<3>({lanes + cb, lanes + 64 + cb, lanes + 128 + cb}, ld);
+        const int left = t < s.N ? np - cb : 0;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (half * 32 + j < np) *out = a0[j] + (a1[j] + a2[j]);
-            out += s.N;
-          }
+        for (int j = 0; j < 16; ++j) {
+          if (j < left) *out = ld[0][j] + (ld[1][j] + ld[2][j]);
+          out += s.N;
+        }
       }
     }
     tc::tc_fence_before();
@@ -455,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) float slog[2][3 * kQ], stail[2][kQ];
   __shared__ uint64_t bar, gbar[2];
   __shared__ uint32_t slot;
-  const int wg = threadIdx.x / kHalf, t = threadIdx.x % kHalf, quad = t >> 5;
+  const int wg = threadIdx.x / kHalf, t = threadIdx.x % kQ, half = threadIdx.x / kQ & 1, quad = t >> 5;
+  const bool leader = threadIdx.x % kHalf == 0;
   uint8_t* qs = align1k(raw);               // [kQ][NB * 64]
   uint8_t* ks = qs + NB * kQ * 128;         // [kQ][NB * 64], then group 0's scores
   uint8_t* Ws = ks + wg * kQ * 256;         // [kQ][kQ]
@@ -507,9 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   if (first.wait()) {
     // the scores above the diagonal blocks are zero for every item
-    for (int cb = quad + 1; cb < 4; ++cb)
+    for (int cb = half; cb < 4; cb += 2)
+      if (cb > quad)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, cb * 4 + i)) = uint4{0, 0, 0, 0};
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, cb * 4 + i)) = uint4{0, 0, 0, 0};
     GroupMmas done{&gbar[wg], 0u, status, wg};
     const ChunkLogs L = logs_view(slog[wg]);
     float* tail = stail[wg];
@@ -518,14 +552,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; it < m.i1; it += 2, buf ^= 1) {
       const int h = m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT, bh = m.b * s.H + h;
       const int np = min(kPT, s.P - p0);
-      L.hi[t] = hi;
-      L.lo[t] = lo;
-      L.eta[t] = eta;
-      tail[t] = ex2((__shfl_sync(~0u, hi, 31) - hi) + (__shfl_sync(~0u, lo, 31) - lo)) * eta;
+      const float tl = ex2((__shfl_sync(~0u, hi, 31) - hi) + (__shfl_sync(~0u, lo, 31) - lo)) * eta;
+      if (half == 0) {
+        L.hi[t] = hi;
+        L.lo[t] = lo;
+        L.eta[t] = eta;
+        tail[t] = tl;
+      }
       const float f = ex2(hi + lo), thi = hi, tlo = lo;
       cp_wait();
       group_publish(wg);  // the item's rows, state and logs are there
-      if (t == 0) {
+      if (leader) {
         mma<kQ, false, kPT, false, 64>(tmem + kYi, qs, Ss, nsteps, false);
         tc::mma_commit(&gbar[wg]);
       }
@@ -534,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fetch_rows(it + 2, buf ^ 1);
       }
 #pragma unroll 1
-      for (int cb = 0; cb < quad; ++cb) {
+      for (int cb = half; cb < quad; cb += 2) {
         float a[32];
         tc::tmem_ld32(lanes + cb * 32, a);
         const float row = ex2((thi - L.hi[cb * 32 + 31]) + (tlo - L.lo[cb * 32 + 31]));
@@ -549,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, cb * 4 + i)) = o[i];
       }
-      {
+      if ((quad & 1) == half) {
         float a[32];
         tc::tmem_ld32(lanes + quad * 32, a);
         uint4 o[4];
@@ -559,27 +596,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float4 uh = *reinterpret_cast<const float4*>(L.hi + u);
           const float4 ul = *reinterpret_cast<const float4*>(L.lo + u);
           const float4 ue = *reinterpret_cast<const float4*>(L.eta + u);
-          const float w0 = d >= 0 ? a[i * 4] * (ex2((thi - uh.x) + (tlo - ul.x)) * ue.x) : 0.f;
-          const float w1 = d >= 1 ? a[i * 4 + 1] * (ex2((thi - uh.y) + (tlo - ul.y)) * ue.y) : 0.f;
-          const float w2 = d >= 2 ? a[i * 4 + 2] * (ex2((thi - uh.z) + (tlo - ul.z)) * ue.z) : 0.f;
-          const float w3 = d >= 3 ? a[i * 4 + 3] * (ex2((thi - uh.w) + (tlo - ul.w)) * ue.w) : 0.f;
+          // (all lanes compute, then the later tokens' are dropped: no branches)
+          const float w0 = a[i * 4] * (ex2((thi - uh.x) + (tlo - ul.x)) * ue.x);
+          const float w1 = a[i * 4 + 1] * (ex2((thi - uh.y) + (tlo - ul.y)) * ue.y);
+          const float w2 = a[i * 4 + 2] * (ex2((thi - uh.z) + (tlo - ul.z)) * ue.z);
+          const float w3 = a[i * 4 + 3] * (ex2((thi - uh.w) + (tlo - ul.w)) * ue.w);
           uint32_t* ow = &o[i >> 1].x + (i & 1) * 2;
-          ow[0] = pack2(w0, w1);
-          ow[1] = pack2(w2, w3);
+          ow[0] = pack2(d >= 0 ? w0 : 0.f, d >= 1 ? w1 : 0.f);
+          ow[1] = pack2(d >= 2 ? w2 : 0.f, d >= 3 ? w3 : 0.f);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, quad * 4 + i)) = o[i];
       }
       group_publish(wg);
       uint8_t* vb = vs + buf * kQ * 128;
-      if (t == 0) mma<kQ, false, kQ, true, 64>(tmem + kYd, Ws, vb, kQ / 16, false);
+      if (leader) mma<kQ, false, kQ, true, 64>(tmem + kYd, Ws, vb, kQ / 16, false);
       if (!done.wait()) break;  // of the state's product: its tile is free
-      if (t == 0) tc::mma_commit(&gbar[wg]);
+      if (leader) tc::mma_commit(&gbar[wg]);
       if (it + 2 < m.i1) fetch_state(it + 2);
       if (!done.wait()) break;
       const float Dh = D ? D[h] : 0.f;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      {
         float yi[32], yd[32];
         tc::tmem_ld32(lanes + kYi + half * 32, yi);
         tc::tmem_ld32(lanes + kYd + half * 32, yd);
@@ -595,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int a = i * 8 + e * 2;
             const float y0 = fmaf(f, yi[a], yd[a]) + Dh * lo_f(xu[e]);
             const float y1 = fmaf(f, yi[a + 1], yd[a + 1]) + Dh * hi_f(xu[e]);
-            ou[e] = t < m.n ? pack2(y0, y1) : 0u;
+            const uint32_t p = pack2(y0, y1);
+            ou[e] = t < m.n ? p : 0u;
           }
           *at = o;  // y takes the place of v
         }
@@ -605,13 +643,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tc_fence_after();
       // whole rows to memory: eight threads a row
       bf16* out = y + ((long long)bh * s.T + m.t0) * s.P + p0;
-      const int j = t & 7;
+      const int j = t & 7, r0 = threadIdx.x % kHalf >> 3, rows = s.T - m.t0;
+      uint4 o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = (t >> 3) + i * 16;
-        if (m.t0 + r < s.T)
-          store8<VEC>(out + (long long)r * s.P + j * 8, *reinterpret_cast<const uint4*>(vb + piece<kQ>(r, j)),
-                      np - j * 8);
+      for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const uint4*>(vb + piece<kQ>(r0, j) + i * 32 * 128);
+      out += (long long)r0 * s.P + j * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (r0 + i * 32 < rows) store8<VEC>(out, o[i], np - j * 8);
+        out += 32 * (long long)s.P;
       }
     }
   }
@@ -639,30 +679,6 @@ __device__ __forceinline__ float column_sums(float (&v)[16], int lane) {
     }
   return v[0] + __shfl_xor_sync(~0u, v[0], 16);
 }
-// 16 columns of this thread's lane from each of two places.
-__device__ __forceinline__ void tmem_ld16x2(uint32_t a, uint32_t b, float (&x)[16], float (&y)[16]) {
-  uint32_t r[16], u[16];
-#define E2TTT_LD16(R, AT)                                                                            \
-  asm volatile(                                                                                      \
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32"                                                       \
-      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"              \
-      : "=r"(R[0]), "=r"(R[1]), "=r"(R[2]), "=r"(R[3]), "=r"(R[4]), "=r"(R[5]), "=r"(R[6]),          \
-        "=r"(R[7]), "=r"(R[8]), "=r"(R[9]), "=r"(R[10]), "=r"(R[11]), "=r"(R[12]), "=r"(R[13]),      \
-        "=r"(R[14]), "=r"(R[15])                                                                     \
-      : "r"(AT)                                                                                      \
-      : "memory")
-  E2TTT_LD16(r, a);
-  E2TTT_LD16(u, b);
-#undef E2TTT_LD16
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    asm volatile("" : "+r"(r[i]), "+r"(u[i]));  // no use of them moves before the wait
-    x[i] = __uint_as_float(r[i]);
-    y[i] = __uint_as_float(u[i]);
-  }
-}
-
 struct GradOut {
   float *dq, *dk;    // [B*G][parts][T][N]: sums over a part's heads, fp32
   bf16 *dq16, *dk16; // the results themselves, where there is one part
@@ -671,13 +687,17 @@ struct GradOut {
 };
 
 // All gradients of one chunk for a run of heads of one group (and their tiles of
-// 64 state rows: `items`). dq and dk add up over the items on chip: the products
-// with the decayed scores in tensor memory, the states' parts in registers (their
-// rows are scaled item by item).
+// 64 state rows: `items`). dq and dk add up over the items in tensor memory: the
+// products with the decayed scores by the MMAs, the states' parts, whose rows are
+// scaled item by item, by loads and stores between them. (In registers they
+// would not fit beside the rest: with most of the SM's L1 taken as shared memory,
+// spilled registers go to L2.)
 //   tensor memory: [0, 256) scratch (S^T dy | X^T v; then q k^T | dy v^T; then the
 //   two parts of dv), [256, 384) dq, [384, 512) dk
-//   shared memory: q, k; v, dy of the item; S and X in three terms, later
-//   overwritten by the two score matrices (X's first term stays)
+//   shared memory: q, k; v of the item, dy of this and of the next; S and X in
+//   three terms, later overwritten by the two score matrices (X's first term stays)
+// What the next item reads comes in under this one: its S and X to registers once
+// the last products are issued, its v and dy once the scores are made.
 template <int NB, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     grad_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,
@@ -689,17 +709,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTerm = NB * kPT * 128;  // bytes of one term of a state
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[3 * kQ];
-  __shared__ float tail[kQ], rows[2][kQ], cols[4][kQ], rdr[2][kQ], src[2][kQ], diag[2][kQ], warp_ip[8];
+  __shared__ __align__(16) float tail[kQ];
+  __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[2][kQ],
+      warp_ip[kThreads / 32];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
   uint8_t* qs = align1k(raw);
   uint8_t* ks = qs + NB * kQ * 128;
   uint8_t* vs = ks + NB * kQ * 128;
-  uint8_t* gs = vs + kQ * 128;
-  uint8_t* W1 = gs + kQ * 128;   // e^{c_t-c_s} q_t.k_s, [t][s]
-  uint8_t* W2 = W1 + kQ * 256;   // e^{c_t-c_s} eta_s dy_t.v_s
-  uint8_t* Xs = W2 + kQ * 256;   // X, first term
-  uint8_t* St = W1;              // S, three terms, and X's second and third, under W1 and W2
+  uint8_t* gb = vs + kQ * 128;       // two of [kQ][64]: dy, by turns
+  uint8_t* W1 = gb + 2 * kQ * 128;   // e^{c_t-c_s} q_t.k_s, [t][s]
+  uint8_t* W2 = W1 + kQ * 256;       // e^{c_t-c_s} eta_s dy_t.v_s
+  uint8_t* Xs = W2 + kQ * 256;       // X, first term
+  uint8_t* St = W1;                  // S, three terms, and X's second and third, under W1 and W2
   const int c = blockIdx.x, bg = blockIdx.y, b = bg / s.G, g = bg - b * s.G, split = blockIdx.z;
   const int HG = s.H / s.G, items = HG * s.NPT, BH = s.B * s.H, t0 = c * kQ;
   const ChunkLogs L = logs_view(slog);
@@ -710,75 +732,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long qo = ((long long)bg * s.T + t0) * s.N;
   load_rows<kQ, NB, VEC>(qs, q + qo, s.N, n, s.N);
   load_rows<kQ, NB, VEC>(ks, k + qo, s.N, n, s.N);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, half = warp >> 2;
+  // A row (token) has four threads, one for each quarter of its columns.
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, part = warp >> 2;
   const int t = quad * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   constexpr uint32_t kDq = 256, kDk = 384;
-  constexpr int HC = NB * 32;  // this thread's columns of dq and dk: [half * HC, half * HC + HC)
+  constexpr int HC = NB * 16;  // a thread's columns of dq and dk: [part * HC, part * HC + HC)
   const int nsteps = (s.N + 15) / 16;
   Mmas done{&bar, 0u, status};
-  float dqa[HC], dka[HC];
-#pragma unroll
-  for (int i = 0; i < HC; ++i) dqa[i] = dka[i] = 0.f;
   bool ok = true;
 
   const int i0 = split * per, i1 = min(items, i0 + per);
+  auto head = [&](int it) { return g * HG + (s.NPT == 1 ? it : it / s.NPT); };
+  auto tile = [&](int it) { return s.NPT == 1 ? 0 : it % s.NPT; };
+  auto fetch_rows = [&](int it, int buf) {
+    const int p0 = tile(it) * kPT, np = min(kPT, s.P - p0);
+    const long long vo = ((long long)(b * s.H + head(it)) * s.T + t0) * s.P + p0;
+    load_rows<kQ, 1, VEC>(vs, v + vo, s.P, n, np);
+    load_rows<kQ, 1, VEC>(gb + buf * kQ * 128, dy + vo, s.P, n, np);
+  };
+  constexpr int kPer = NB * 8, kStep = kThreads / kPer, kIt = kPT / kStep;
+  float Sf[kIt][8], Xf[kIt][8];
+  auto fetch_states = [&](int it) {
+    const int p0 = tile(it) * kPT, np = min(kPT, s.P - p0), j = threadIdx.x % kPer, r0 = threadIdx.x / kPer;
+    const long long so = (((long long)c * BH + b * s.H + head(it)) * s.P + p0 + r0) * s.N + j * 8;
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const int left = r0 + i * kStep < np ? s.N - j * 8 : 0;
+      load8f<VEC>(Sf[i], states + so + (long long)i * kStep * s.N, left);
+      load8f<VEC>(Xf[i], ends + so + (long long)i * kStep * s.N, left);
+    }
+  };
+  fetch_rows(i0, 0);
+  fetch_states(i0);
 #pragma unroll 1
   for (int it = i0; it < i1 && ok; ++it) {
-    const int h = g * HG + it / s.NPT, pt = it % s.NPT, bh = b * s.H + h;
+    const int h = head(it), pt = tile(it), bh = b * s.H + h;
     const int p0 = pt * kPT, np = min(kPT, s.P - p0);
     const long long vo = ((long long)bh * s.T + t0) * s.P + p0;
-    load_rows<kQ, 1, VEC>(vs, v + vo, s.P, n, np);
-    load_rows<kQ, 1, VEC>(gs, dy + vo, s.P, n, np);
+    uint8_t* gs = gb + ((it - i0) & 1) * kQ * 128;
     load_logs(L, logs, bh, s.NC, c);
-    // S and X, as three terms each, and <S, X>: two batches of loads, so that a
-    // batch is in flight at once
+    // S and X, as three terms each, and <S, X>
     {
-      constexpr int kPer = NB * 8, kStep = kThreads / kPer, kIt = kPT / kStep;
-      const long long so = (((long long)c * BH + bh) * s.P + p0) * s.N;
       const int j = threadIdx.x % kPer, r0 = threadIdx.x / kPer;
       float ip = 0.f;
 #pragma unroll
-      for (int i0 = 0; i0 < kIt; i0 += 2) {
-        float f[2][8], x[2][8];
+      for (int i = 0; i < kIt; ++i) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int p = r0 + (i0 + i) * kStep;
-          load8f<VEC>(f[i], states + so + (long long)p * s.N + j * 8, p < np ? s.N - j * 8 : 0);
-          load8f<VEC>(x[i], ends + so + (long long)p * s.N + j * 8, p < np ? s.N - j * 8 : 0);
-        }
+        for (int e = 0; e < 8; ++e) ip = fmaf(Sf[i][e], Xf[i][e], ip);
+        const uint32_t at = piece<kPT>(r0 + i * kStep, j);
+        uint4 term[3];
+        split3(Sf[i], term);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ip = fmaf(f[i][e], x[i][e], ip);
-          const uint32_t at = piece<kPT>(r0 + (i0 + i) * kStep, j);
-          uint4 term[3];
-          split3(f[i], term);
-#pragma unroll
-          for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4*>(St + m * kTerm + at) = term[m];
-          split3(x[i], term);
-          *reinterpret_cast<uint4*>(Xs + at) = term[0];
-          *reinterpret_cast<uint4*>(St + 3 * kTerm + at) = term[1];
-          *reinterpret_cast<uint4*>((NB == 1 ? St + 4 * kTerm : Xs + kTerm) + at) = term[2];
-        }
+        for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4*>(St + m * kTerm + at) = term[m];
+        split3(Xf[i], term);
+        *reinterpret_cast<uint4*>(Xs + at) = term[0];
+        *reinterpret_cast<uint4*>(St + 3 * kTerm + at) = term[1];
+        *reinterpret_cast<uint4*>((NB == 1 ? St + 4 * kTerm : Xs + kTerm) + at) = term[2];
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) ip += __shfl_xor_sync(~0u, ip, d);
       if (lane == 0) warp_ip[warp] = ip;
-    }
-    if (it + 1 < i1) {
-      // the next item's rows and states into L2 while this one computes
-      const int h2 = g * HG + (it + 1) / s.NPT, q0 = (it + 1) % s.NPT * kPT, bh2 = b * s.H + h2;
-      const long long v2 = ((long long)bh2 * s.T + t0) * s.P + q0;
-      const long long s2 = (((long long)c * BH + bh2) * s.P + q0) * s.N;
-      const int room = min(kPT, s.P - q0);
-      if (threadIdx.x < n) prefetch_l2(v + v2 + (long long)threadIdx.x * s.P);
-      if (threadIdx.x >= 128 && threadIdx.x - 128 < n) prefetch_l2(dy + v2 + (long long)(threadIdx.x - 128) * s.P);
-      const int line = threadIdx.x * 32;  // of the tile's room * N values
-      if (line < room * s.N) {
-        prefetch_l2(states + s2 + line);
-        prefetch_l2(ends + s2 + line);
-      }
     }
     cp_wait();
     publish();
@@ -794,41 +808,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!(ok = done.wait())) break;
     // the states' parts of dq and dk, and their dots with q and k
     {
-      const float f = L.from_start(t), e = L.to_end(t), eta = L.eta[t];
+      const float f = L.from_start(t), e = L.to_end(t), ee = e * L.eta[t];
+      const bool add = it > i0;
       float rd = 0.f, sd = 0.f;
 #pragma unroll
       for (int cb = 0; cb < NB; ++cb) {
-        float a[32];
+        const uint32_t col = lanes + part * HC + cb * 16;
+        float ld[4][16];
+        tmem_ld16<4>({col, col + 128, col + kDq, col + kDk}, ld);
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          tc::tmem_ld32(lanes + which * 128 + half * HC + cb * 32, a);
-          const uint8_t* tile = which ? ks : qs;
-          const float scale = which ? e : f;
-          float dot = 0.f;
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t at = piece<kQ>(t, (part * HC + cb * 16) / 8 + j);
+          const uint4 rq = *reinterpret_cast<const uint4*>(qs + at), rk = *reinterpret_cast<const uint4*>(ks + at);
+          const uint32_t *uq = &rq.x, *uk = &rk.x;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 r = *reinterpret_cast<const uint4*>(tile + piece<kQ>(t, (half * HC + cb * 32) / 8 + j));
-            const uint32_t* u = &r.x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = j * 8 + i * 2;
-              dot = fmaf(a[at], lo_f(u[i]), dot);
-              dot = fmaf(a[at + 1], hi_f(u[i]), dot);
-            }
-          }
-          if (which) {
-            sd = fmaf(dot, scale, sd);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) dka[cb * 32 + i] = fmaf(a[i], scale * eta, dka[cb * 32 + i]);
-          } else {
-            rd = fmaf(dot, scale, rd);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) dqa[cb * 32 + i] = fmaf(a[i], scale, dqa[cb * 32 + i]);
+          for (int i = 0; i < 4; ++i) {
+            const int c0 = j * 8 + i * 2;
+            rd = fmaf(ld[0][c0], lo_f(uq[i]), rd);
+            sd = fmaf(ld[1][c0], lo_f(uk[i]), sd);
+            rd = fmaf(ld[0][c0 + 1], hi_f(uq[i]), rd);
+            sd = fmaf(ld[1][c0 + 1], hi_f(uk[i]), sd);
           }
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          ld[2][i] = fmaf(ld[0][i], f, add ? ld[2][i] : 0.f);
+          ld[3][i] = fmaf(ld[1][i], ee, add ? ld[3][i] : 0.f);
+        }
+        tmem_st16(col + kDq, ld[2]);
+        tmem_st16(col + kDk, ld[3]);
       }
-      rdr[half][t] = rd;
-      src[half][t] = sd;
+      rdr[part][t] = rd * f;
+      src[part][t] = sd * e;
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -839,121 +850,170 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mma_commit(&bar);
     }
     if (!(ok = done.wait())) break;
+    if (it + 1 < i1) fetch_rows(it + 1, (it - i0 + 1) & 1);  // v has done its part
     // the decayed scores, and the row and column sums of Z off its diagonal
-    float zrow = 0.f;
-#pragma unroll 1
-    for (int cb = half; cb < 4; cb += 2) {
-#pragma unroll 1
-      for (int sub = 0; sub < 2; ++sub) {
-        const int u0 = cb * 32 + sub * 16;
-        uint4 o1[2] = {}, o2[2] = {};
-        if (cb <= quad) {
-          float m[16], kk[16], off[16];
-          tmem_ld16x2(lanes + u0, lanes + 128 + u0, m, kk);
-          const float rowf = cb < quad ? L.decay(t, cb * 32 + 31) : 0.f;
+    float zrow = 0.f, dr = 0.f, dd = 0.f;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const int u0 = part * 32 + sub * 16;
+      uint4 o1[2] = {}, o2[2] = {};
+      if (part <= quad) {
+        float ld[2][16], off[16];
+        tmem_ld16<2>({lanes + u0, lanes + 128 + u0}, ld);
+        float(&m)[16] = ld[0], (&kk)[16] = ld[1];
+        float e[16], h[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v4 = *reinterpret_cast<const float4*>(L.eta + u0 + i * 4);
+          h[i * 4] = v4.x, h[i * 4 + 1] = v4.y, h[i * 4 + 2] = v4.z, h[i * 4 + 3] = v4.w;
+        }
+        if (part < quad) {
+          const float row = L.decay(t, part * 32 + 31);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v4 = *reinterpret_cast<const float4*>(tail + u0 + i * 4);
+            e[i * 4] = row * v4.x, e[i * 4 + 1] = row * v4.y, e[i * 4 + 2] = row * v4.z, e[i * 4 + 3] = row * v4.w;
+          }
+        } else {
+          const float thi = L.hi[t], tlo = L.lo[t];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 a4 = *reinterpret_cast<const float4*>(L.hi + u0 + i * 4);
+            const float4 b4 = *reinterpret_cast<const float4*>(L.lo + u0 + i * 4);
+            e[i * 4] = ex2((thi - a4.x) + (tlo - b4.x));
+            e[i * 4 + 1] = ex2((thi - a4.y) + (tlo - b4.y));
+            e[i * 4 + 2] = ex2((thi - a4.z) + (tlo - b4.z));
+            e[i * 4 + 3] = ex2((thi - a4.w) + (tlo - b4.w));
+          }
+          // the later tokens' are dropped (all lanes compute: no branches)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int u = u0 + i;
-            const float e = cb < quad ? rowf * tail[u] : u <= t ? L.decay(t, u) : 0.f;
-            const float a = u <= t ? e * m[i] : 0.f, d = u <= t ? kk[i] : 0.f;
-            const float r = a * d;
-            if (u == t) {
-              diag[0][t] = r;
-              diag[1][t] = d;
-            }
-            off[i] = u < t ? r : 0.f;
-            zrow = fmaf(off[i], L.eta[u], zrow);
-            m[i] = a;
-            kk[i] = d * (e * L.eta[u]);
+            e[i] = u <= t ? e[i] : 0.f;
+            m[i] = u <= t ? m[i] : 0.f;
+            kk[i] = u <= t ? kk[i] : 0.f;
           }
-          uint32_t *w1 = &o1[0].x, *w2 = &o2[0].x;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            w1[i] = pack2(m[2 * i], m[2 * i + 1]);
-            w2[i] = pack2(kk[2 * i], kk[2 * i + 1]);
-          }
-          const float sum = column_sums(off, lane);
-          if (lane < 16) cols[quad][u0 + lane] = sum;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          *reinterpret_cast<uint4*>(W1 + piece<kQ>(t, u0 / 8 + i)) = o1[i];
-          *reinterpret_cast<uint4*>(W2 + piece<kQ>(t, u0 / 8 + i)) = o2[i];
+        for (int i = 0; i < 16; ++i) {
+          m[i] *= e[i];
+          off[i] = m[i] * kk[i];
         }
+        if (part == quad)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const bool on = u0 + i == t;
+            dr = on ? off[i] : dr;
+            dd = on ? kk[i] : dd;
+            off[i] = on ? 0.f : off[i];
+          }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) kk[i] *= e[i] * h[i];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zrow = fmaf(off[i], h[i], zrow);
+        uint32_t *w1 = &o1[0].x, *w2 = &o2[0].x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          w1[i] = pack2(m[2 * i], m[2 * i + 1]);
+          w2[i] = pack2(kk[2 * i], kk[2 * i + 1]);
+        }
+        const float sum = column_sums(off, lane);
+        if (lane < 16) cols[quad][u0 + lane] = sum;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<uint4*>(W1 + piece<kQ>(t, u0 / 8 + i)) = o1[i];
+        *reinterpret_cast<uint4*>(W2 + piece<kQ>(t, u0 / 8 + i)) = o2[i];
       }
     }
-    rows[half][t] = zrow;
+    rows[part][t] = zrow;
+    if (part == quad) {  // the quarter that holds this row's diagonal block
+      diag[0][t] = dr;
+      diag[1][t] = dd;
+    }
     publish();
     if (threadIdx.x == 0) {
       mma<kQ, true, kQ, true, 64>(tmem, W1, gs, kQ / 16, false);
       mma<kQ, false, kPT, false, 64>(tmem + 64, ks, Xs, nsteps, false);
-      mma<kQ, false, kQ, true, NB * 64>(tmem + kDq, W2, ks, kQ / 16, it > i0);
-      mma<kQ, true, kQ, true, NB * 64>(tmem + kDk, W2, qs, kQ / 16, it > i0);
+      mma<kQ, false, kQ, true, NB * 64>(tmem + kDq, W2, ks, kQ / 16, true);
+      mma<kQ, true, kQ, true, NB * 64>(tmem + kDk, W2, qs, kQ / 16, true);
       tc::mma_commit(&bar);
     }
-    if (warp == 0) {
+    if (it + 1 < i1) fetch_states(it + 1);
+    if (warp == kThreads / 32 - 1) {
       // ddt, dA, dD: lane l has the tokens 4 l .. 4 l + 3
-      double a4[4], b4[4], as = 0.0, bs = 0.0;
-      float off4[4], src4[4], dd = 0.f, ip = 0.f;
+      float a4[4], b4[4], off4[4], src4[4], as = 0.f, bs = 0.f, dsum = 0.f;
+      float ip = lane < kThreads / 32 ? warp_ip[lane] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ip += warp_ip[i];
+      for (int d = kThreads / 64; d; d >>= 1) ip += __shfl_xor_sync(~0u, ip, d);
+      ip = __shfl_sync(~0u, ip, 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = lane * 4 + i;
         float off = 0.f;
-        for (int qd = r >> 5; qd < 4; ++qd) off += cols[qd][r];
+#pragma unroll
+        for (int qd = 0; qd < 4; ++qd) off += qd >= r >> 5 ? cols[qd][r] : 0.f;
         off4[i] = off;
-        src4[i] = src[0][r] + src[1][r];
-        a4[i] = (double)(rows[0][r] + rows[1][r]) - (double)(L.eta[r] * off) + (double)(rdr[0][r] + rdr[1][r]);
-        b4[i] = (double)L.eta[r] * src4[i];
+        src4[i] = (src[0][r] + src[1][r]) + (src[2][r] + src[3][r]);
+        a4[i] = ((rows[0][r] + rows[1][r]) + (rows[2][r] + rows[3][r]) - L.eta[r] * off) +
+                ((rdr[0][r] + rdr[1][r]) + (rdr[2][r] + rdr[3][r]));
+        b4[i] = L.eta[r] * src4[i];
         as += a4[i];
         bs += b4[i];
-        dd += diag[1][r];
+        dsum += diag[1][r];
       }
-      double after = as, before = bs;  // of this lane's tokens on; up to them
+      float after = as, before = bs;  // of this lane's tokens on; up to them
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const double x = __shfl_down_sync(~0u, after, d), y = __shfl_up_sync(~0u, before, d);
-        if (lane + d < 32) after += x;
-        if (lane >= d) before += y;
+        const float x = __shfl_down_sync(~0u, after, d), y = __shfl_up_sync(~0u, before, d);
+        after += lane + d < 32 ? x : 0.f;
+        before += lane >= d ? y : 0.f;
       }
-      before -= bs;
-      const double through = (double)L.from_start(kQ - 1) * ip;
-      const float Ah = A[h];
-      double dA = 0.0;
+      // exclusive of this lane's own, without taking them off again
+      after = __shfl_down_sync(~0u, after, 1);
+      before = __shfl_up_sync(~0u, before, 1);
+      after = lane < 31 ? after : 0.f;
+      before = lane > 0 ? before : 0.f;
+      const float through = L.from_start(kQ - 1) * ip, Ah = A[h];
+      float dl[4], dA = 0.f;
+#pragma unroll
+      for (int i = 3; i >= 0; --i) dl[i] = after += a4[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dl[i] += before + through;
+        before += b4[i];
+      }
       float* out = o.ddt + ((long long)pt * BH + bh) * s.T + t0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = lane * 4 + i;
-        const double dl = after + before + through;
-        after -= a4[i];
-        before += b4[i];
-        dA += L.eta[r] * dl;
-        if (t0 + r < s.T) out[r] = r < n ? (float)(Ah * dl + off4[i] + diag[0][r] + src4[i]) : 0.f;
+        dA = fmaf(L.eta[r], dl[i], dA);
+        const float x = fmaf(Ah, dl[i], off4[i] + diag[0][r] + src4[i]);
+        if (t0 + r < s.T) out[r] = r < n ? x : 0.f;
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) {
         dA += __shfl_xor_sync(~0u, dA, d);
-        dd += __shfl_xor_sync(~0u, dd, d);
+        dsum += __shfl_xor_sync(~0u, dsum, d);
       }
       if (lane == 0) {
         const long long at = ((long long)c * s.NPT + pt) * BH + bh;
-        o.dA[at] = (float)dA;
-        o.dD[at] = dd;
+        o.dA[at] = dA;
+        o.dD[at] = dsum;
       }
       __syncwarp();
     }
     if (!(ok = done.wait())) break;
     {
-      float a1[32], a2[32];
-      tc::tmem_ld32(lanes + half * 32, a1);
-      tc::tmem_ld32(lanes + 64 + half * 32, a2);
+      float ld[2][16];
+      tmem_ld16<2>({lanes + part * 16, lanes + 64 + part * 16}, ld);
+      float(&a1)[16] = ld[0], (&a2)[16] = ld[1];
       const float e = L.to_end(t), eta = L.eta[t], Dh = D ? D[h] : 0.f;
-      bf16* out = o.dv + vo + (long long)t * s.P + half * 32;
+      bf16* out = o.dv + vo + (long long)t * s.P + part * 16;
       if (t0 + t < s.T)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 r = *reinterpret_cast<const uint4*>(gs + piece<kQ>(t, half * 4 + i));
+        for (int i = 0; i < 2; ++i) {
+          const uint4 r = *reinterpret_cast<const uint4*>(gs + piece<kQ>(t, part * 2 + i));
           const uint32_t* u = &r.x;
           uint4 w;
           uint32_t* wu = &w.x;
@@ -962,9 +1022,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int x = i * 8 + j * 2;
             const float d0 = fmaf(eta, fmaf(e, a2[x], a1[x]), Dh * lo_f(u[j]));
             const float d1 = fmaf(eta, fmaf(e, a2[x + 1], a1[x + 1]), Dh * hi_f(u[j]));
-            wu[j] = t < n ? pack2(d0, d1) : 0u;
+            const uint32_t p = pack2(d0, d1);
+            wu[j] = t < n ? p : 0u;
           }
-          store8<VEC>(out + i * 8, w, np - (half * 32 + i * 8));
+          store8<VEC>(out + i * 8, w, np - (part * 16 + i * 8));
         }
     }
     tc::tc_fence_before();
@@ -978,30 +1039,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int which = 0; which < 2; ++which)
 #pragma unroll
       for (int cb = 0; cb < NB; ++cb) {
-        float a[32];
-        tc::tmem_ld32(lanes + (which ? kDk : kDq) + half * HC + cb * 32, a);
+        float ld[1][16];
+        tmem_ld16<1>({lanes + (which ? kDk : kDq) + part * HC + cb * 16}, ld);
+        float(&a)[16] = ld[0];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) a[i] = t < n ? a[i] + (which ? dka : dqa)[cb * 32 + i] : 0.f;
-        const int col = half * HC + cb * 32;
+        for (int i = 0; i < 16; ++i) {
+          a[i] = t < n ? a[i] : 0.f;
+        }
+        const int col = part * HC + cb * 16;
         if (!there) continue;
         if (parts == 1) {
           bf16* out = (which ? o.dk16 : o.dq16) + qo + (long long)t * s.N + col;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
             store8<VEC>(out + i * 8,
-                   uint4{pack2(a[i * 8], a[i * 8 + 1]), pack2(a[i * 8 + 2], a[i * 8 + 3]),
-                         pack2(a[i * 8 + 4], a[i * 8 + 5]), pack2(a[i * 8 + 6], a[i * 8 + 7])},
-                   s.N - col - i * 8);
+                        uint4{pack2(a[i * 8], a[i * 8 + 1]), pack2(a[i * 8 + 2], a[i * 8 + 3]),
+                              pack2(a[i * 8 + 4], a[i * 8 + 5]), pack2(a[i * 8 + 6], a[i * 8 + 7])},
+                        s.N - col - i * 8);
         } else {
           float* out = (which ? o.dk : o.dq) + (((long long)bg * parts + split) * s.T + t0 + t) * s.N + col;
           if (s.N % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
               if (col + i * 4 < s.N)
                 *reinterpret_cast<float4*>(out + i * 4) = float4{a[i * 4], a[i * 4 + 1], a[i * 4 + 2], a[i * 4 + 3]};
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 16; ++i)
               if (col + i < s.N) out[i] = a[i];
           }
         }
@@ -1018,7 +1082,7 @@ size_t out_smem() {
 
 template <int NB>
 size_t grad_smem() {
-  return 1024 + 2 * NB * kQ * 128 + 2 * kQ * 128 + 2 * kQ * 256 + (NB == 1 ? 1 : 2) * NB * kPT * 128;
+  return 1024 + 2 * NB * kQ * 128 + 3 * kQ * 128 + 2 * kQ * 256 + (NB == 1 ? 1 : 2) * NB * kPT * 128;
 }
 
 // How many blocks share the items of a group's chunk: of all ways, the one whose

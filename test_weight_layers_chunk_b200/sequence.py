@@ -13,11 +13,12 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 from array import array
 
 import torch
 
-from . import (BF16, ERR_INVALID_ARG, E2TTTError, F32, _check, _lib, _P, _ptr, _stream)
+from . import BF16, ERR_INVALID_ARG, OK, E2TTTError, F32, _check, _lib, _P, _ptr, _stream
 
 
 class e2ttt_conv_shape(ctypes.Structure):
@@ -168,80 +169,125 @@ def _refuse(what):
     raise E2TTTError(ERR_INVALID_ARG, what)
 
 
-def _need(name, t, shape, dtype, device):
-    """t is a contiguous CUDA tensor of this shape, type and device."""
-    if not isinstance(t, torch.Tensor):
+def _need(name, t, shape, dtype, dev):
+    """t is a contiguous tensor of this shape and type on CUDA device number dev."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
         _refuse(f"{name} must be a tensor, got {type(t).__name__}")
     if t.shape != shape:
         _refuse(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         _refuse(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        _refuse(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        _refuse(f"{name} must be contiguous")
-
-
-def _may(name, t, shape, dtype, device):
-    if t is not None:
-        _need(name, t, shape, dtype, device)
+    if t.get_device() != dev:
+        _refuse(f"{name} must be on cuda:{dev}, got {t.device}")
+    _refuse(f"{name} must be contiguous")
 
 
 def _first(name, t, dims):
-    """The tensor that fixes sizes, type and device."""
+    """The tensor that fixes sizes, type and device; returns its device's number
+    and its type's code."""
     if not isinstance(t, torch.Tensor) or t.dim() != dims:
         _refuse(f"{name} must be a tensor of {dims} dimensions")
     if not t.is_cuda:
         _refuse(f"{name} must be on a CUDA device, got {t.device}")
-    if t.dtype not in _ACT:
+    act = _ACT.get(t.dtype)
+    if act is None:
         _refuse(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous")
+    return t.get_device(), act
+
+
+def _dims(name, t, dims, what):
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        _refuse(f"{name} must be {what}")
 
 
 @contextlib.contextmanager
-def _guard(device, stream):
-    with torch.cuda.device(device):
+def _guard(dev, stream):
+    """Makes device number `dev` current, and `stream` where one is given."""
+    with torch.cuda.device(dev):
         if stream is None:
             yield
         else:
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            elif stream.device != device:
-                _refuse(f"the stream is on {stream.device}, the tensors are on {device}")
+                stream = torch.cuda.ExternalStream(stream, device=dev)
+            elif stream.device.index != dev:
+                _refuse(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
             with torch.cuda.stream(stream):
                 yield
 
 
-_HERE = contextlib.nullcontext()
+def _elsewhere(dev, stream):
+    """Whether the call has to change the current device or stream first."""
+    return stream is not None or torch.cuda.current_device() != dev
 
 
-def _on(device, stream):
-    """Makes `device` current, and `stream` where one is given."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return _HERE
-    return _guard(device, stream)
+# The current stream's handle, by the short way where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _scratch(ws, need, device):
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(fn, *args):
+    st = fn(*args)
+    if st != OK:
+        _check(st)
+
+
+def _scratch(ws, need, like):
+    """The caller's workspace or a new one; (its pointer, its size, what keeps it)."""
     if ws is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous():
-        _refuse(f"ws must be a contiguous tensor on {device}")
-    return ws
+        ws = like.new_empty(need, dtype=torch.uint8)
+        return ws.data_ptr(), need, ws
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != like.get_device() or not ws.is_contiguous():
+        _refuse(f"ws must be a contiguous tensor on {like.device}")
+    return ws.data_ptr(), _nbytes(ws), ws
+
+
+# Shapes and the sizes that follow from them, by value.
+@functools.lru_cache(maxsize=1024)
+def _conv_shape(*sizes):
+    shape = e2ttt_conv_shape(*sizes)
+    return ctypes.byref(shape), e2ttt_short_conv_workspace_bytes(shape)
+
+
+@functools.lru_cache(maxsize=1024)
+def _ssm_shape(*sizes):
+    shape = e2ttt_ssm_shape(*sizes)
+    return (ctypes.byref(shape), e2ttt_ssm_workspace_bytes(shape, 0), e2ttt_ssm_workspace_bytes(shape, 1),
+            e2ttt_ssm_saved_bytes(shape))
+
+
+def _known(sizes_of, *sizes):
+    found = sizes_of(*sizes)
+    if found[1] == 0:  # a shape the library refuses: asked again, it says why
+        sizes_of.__wrapped__(*sizes)
+        _check(ERR_INVALID_ARG)
+    return found
 
 
 # ---------------------------------------------------------------- short convolution
 def _conv_check(x, w, bias, state, lengths, silu):
+    dev, act = _first("x", x, 4)
+    _dims("w", w, 3, "[H, d, W]")
     B, H, T, d = x.shape
-    if not isinstance(w, torch.Tensor) or w.dim() != 3:
-        _refuse("w must be [H, d, W]")
     W = w.shape[2]
-    dev, f32 = x.device, torch.float32
-    _need("x", x, x.shape, x.dtype, dev)
+    f32 = torch.float32
     _need("w", w, (H, d, W), f32, dev)
-    _may("bias", bias, (H, d), f32, dev)
-    _may("state", state, (B, H, W - 1, d), x.dtype, dev)
-    _may("lengths", lengths, (B,), torch.int32, dev)
-    return e2ttt_conv_shape(B, H, T, d, W, _ACT[x.dtype], 1 if silu else 0)
+    if bias is not None:
+        _need("bias", bias, (H, d), f32, dev)
+    if state is not None:
+        _need("state", state, (B, H, W - 1, d), x.dtype, dev)
+    if lengths is not None:
+        _need("lengths", lengths, (B,), torch.int32, dev)
+    shape, need = _known(_conv_shape, B, H, T, d, W, act, 1 if silu else 0)
+    return dev, shape, need, (B, H, W - 1, d)
 
 
 def short_conv_fwd(x, w, bias=None, state=None, lengths=None, *, silu=True, return_state=False,
@@ -250,13 +296,14 @@ def short_conv_fwd(x, w, bias=None, state=None, lengths=None, *, silu=True, retu
     [H, d, W] and bias [H, d] fp32, state [B, H, W-1, d] (the inputs before the
     first token; None: zeros), lengths int32 [B] (a padded batch). Returns (y,
     state_end), state_end None unless return_state."""
-    _first("x", x, 4)
-    shape = _conv_check(x, w, bias, state, lengths, silu)
-    with _on(x.device, stream):
-        y = torch.empty_like(x)
-        end = (torch.empty((shape.B, shape.H, shape.W - 1, shape.d), dtype=x.dtype, device=x.device)
-               if return_state else None)
-        e2ttt_short_conv_fwd(shape, x, w, bias, state, lengths, y, end)
+    dev, shape, _, history = _conv_check(x, w, bias, state, lengths, silu)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return short_conv_fwd(x, w, bias, state, lengths, silu=silu, return_state=return_state)
+    y = torch.empty_like(x)
+    end = x.new_empty(history) if return_state else None
+    _run(_lib.e2ttt_short_conv_fwd, shape, x.data_ptr(), w.data_ptr(), _p(bias), _p(state), _p(lengths),
+         y.data_ptr(), _p(end), _raw_stream(dev))
     return y, end
 
 
@@ -264,65 +311,63 @@ def short_conv_bwd(x, w, dy, bias=None, state=None, dstate_end=None, lengths=Non
                    ws=None, stream=None):
     """Gradients of short_conv_fwd for <dy, y> + <dstate_end, state_end>: a dict
     dx, dw, dbias (None without bias), dstate (None without state)."""
-    _first("x", x, 4)
-    shape = _conv_check(x, w, bias, state, lengths, silu)
-    dev = x.device
+    dev, shape, need, history = _conv_check(x, w, bias, state, lengths, silu)
     _need("dy", dy, x.shape, x.dtype, dev)
-    _may("dstate_end", dstate_end, (shape.B, shape.H, shape.W - 1, shape.d), x.dtype, dev)
-    with _on(dev, stream):
-        g = dict(dx=torch.empty_like(x), dw=torch.empty_like(w),
-                 dbias=None if bias is None else torch.empty_like(bias),
-                 dstate=None if state is None else torch.empty_like(state))
-        ws = _scratch(ws, _bytes(e2ttt_short_conv_workspace_bytes(shape)), dev)
-        e2ttt_short_conv_bwd(shape, x, w, bias, state, lengths, dy, dstate_end, g["dx"], g["dw"],
-                             g["dbias"], g["dstate"], ws)
-    return g
+    if dstate_end is not None:
+        _need("dstate_end", dstate_end, history, x.dtype, dev)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return short_conv_bwd(x, w, dy, bias, state, dstate_end, lengths, silu=silu, ws=ws)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dstate = None if state is None else torch.empty_like(state)
+    wp, wn, _keep = _scratch(ws, need, x)
+    _run(_lib.e2ttt_short_conv_bwd, shape, x.data_ptr(), w.data_ptr(), _p(bias), _p(state), _p(lengths),
+         dy.data_ptr(), _p(dstate_end), dx.data_ptr(), dw.data_ptr(), _p(dbias), _p(dstate), wp, wn,
+         _raw_stream(dev))
+    return dict(dx=dx, dw=dw, dbias=dbias, dstate=dstate)
 
 
 def short_conv_step(x, state, w, bias=None, *, silu=True, out=None, stream=None):
     """One token per row: x [B, H, d], state [B, H, W-1, d] updated in place.
     Returns y [B, H, d] (`out` where given)."""
-    _first("x", x, 3)
+    dev, act = _first("x", x, 3)
+    _dims("w", w, 3, "[H, d, W]")
     B, H, d = x.shape
-    dev = x.device
-    if not isinstance(w, torch.Tensor) or w.dim() != 3:
-        _refuse("w must be [H, d, W]")
     W = w.shape[2]
-    _need("x", x, x.shape, x.dtype, dev)
     _need("w", w, (H, d, W), torch.float32, dev)
-    _may("bias", bias, (H, d), torch.float32, dev)
+    if bias is not None:
+        _need("bias", bias, (H, d), torch.float32, dev)
     _need("state", state, (B, H, W - 1, d), x.dtype, dev)
-    _may("out", out, x.shape, x.dtype, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty_like(x)
-        e2ttt_short_conv_step(e2ttt_conv_shape(B, H, 1, d, W, _ACT[x.dtype], 1 if silu else 0), x, w,
-                              bias, state, out)
+    if out is not None:
+        _need("out", out, x.shape, x.dtype, dev)
+    shape, _ = _known(_conv_shape, B, H, 1, d, W, act, 1 if silu else 0)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return short_conv_step(x, state, w, bias, silu=silu, out=out)
+    if out is None:
+        out = torch.empty_like(x)
+    _run(_lib.e2ttt_short_conv_step, shape, x.data_ptr(), w.data_ptr(), _p(bias), state.data_ptr(),
+         out.data_ptr(), _raw_stream(dev))
     return out
 
 
 # ---------------------------------------------------------------- state-space scan
 def _ssm_check(q, k, v, dt, A, D, lengths):
+    dev, act = _first("v", v, 4)
+    _dims("q", q, 4, "[B, G, T, d_k]")
     B, H, T, d_v = v.shape
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        _refuse("q must be [B, G, T, d_k]")
     G, d_k = q.shape[1], q.shape[3]
-    dev, f32 = v.device, torch.float32
-    _need("v", v, v.shape, v.dtype, dev)
-    _need("q", q, (B, G, T, d_k), v.dtype, dev)
-    _need("k", k, (B, G, T, d_k), v.dtype, dev)
+    f32, qk = torch.float32, (B, G, T, d_k)
+    _need("q", q, qk, v.dtype, dev)
+    _need("k", k, qk, v.dtype, dev)
     _need("dt", dt, (B, H, T), f32, dev)
     _need("A", A, (H,), f32, dev)
-    _may("D", D, (H,), f32, dev)
-    _may("lengths", lengths, (B,), torch.int32, dev)
-    return e2ttt_ssm_shape(B, H, G, T, d_k, d_v, _ACT[v.dtype])
-
-
-def _bytes(n):
-    """A workspace size; 0 stands for a shape the library refuses, and it says why."""
-    if n == 0:
-        _check(ERR_INVALID_ARG)
-    return n
+    if D is not None:
+        _need("D", D, (H,), f32, dev)
+    if lengths is not None:
+        _need("lengths", lengths, (B,), torch.int32, dev)
+    return dev, _known(_ssm_shape, B, H, G, T, d_k, d_v, act), (B, H, d_v, d_k)
 
 
 def ssm_scan_fwd(q, k, v, dt, A, D=None, S0=None, lengths=None, *, save_states=False, ws=None,
@@ -332,19 +377,19 @@ def ssm_scan_fwd(q, k, v, dt, A, D=None, S0=None, lengths=None, *, save_states=F
     fp32; H / G heads share a group), dt [B, H, T], A and D [H], S0
     [B, H, d_v, d_k] fp32, lengths int32 [B] (a padded batch). Returns (y, S_end,
     saved), saved (what ssm_scan_bwd needs) None unless save_states."""
-    _first("v", v, 4)
-    shape = _ssm_check(q, k, v, dt, A, D, lengths)
-    dev = v.device
-    state = (shape.B, shape.H, shape.d_v, shape.d_k)
-    _may("S0", S0, state, torch.float32, dev)
-    with _on(dev, stream):
-        need = _bytes(e2ttt_ssm_workspace_bytes(shape, 0))
-        y = torch.empty_like(v)
-        S_end = torch.empty(state, dtype=torch.float32, device=dev)
-        saved = (torch.empty(e2ttt_ssm_saved_bytes(shape) // 4, dtype=torch.float32, device=dev)
-                 if save_states else None)
-        e2ttt_ssm_scan_fwd(shape, q, k, v, dt, A, D, S0, lengths, y, S_end, saved,
-                           _scratch(ws, need, dev))
+    dev, (shape, need, _, n_saved), state = _ssm_check(q, k, v, dt, A, D, lengths)
+    if S0 is not None:
+        _need("S0", S0, state, torch.float32, dev)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return ssm_scan_fwd(q, k, v, dt, A, D, S0, lengths, save_states=save_states, ws=ws)
+    y = torch.empty_like(v)
+    S_end = dt.new_empty(state)
+    saved = dt.new_empty(n_saved // 4) if save_states else None
+    wp, wn, _keep = _scratch(ws, need, v)
+    _run(_lib.e2ttt_ssm_scan_fwd, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(),
+         A.data_ptr(), _p(D), _p(S0), _p(lengths), y.data_ptr(), S_end.data_ptr(), _p(saved), wp, wn,
+         _raw_stream(dev))
     return y, S_end, saved
 
 
@@ -353,62 +398,73 @@ def ssm_scan_bwd(q, k, v, dt, A, saved, dy, D=None, dS_end=None, lengths=None, *
     """Gradients of ssm_scan_fwd for <dy, y> + <dS_end, S_end>: a dict dq, dk, dv,
     ddt, dA, dD (None without D), dS0. `saved` is the forward's; lengths must be
     the forward's too."""
-    _first("v", v, 4)
-    shape = _ssm_check(q, k, v, dt, A, D, lengths)
-    dev, f32 = v.device, torch.float32
-    state = (shape.B, shape.H, shape.d_v, shape.d_k)
+    dev, (shape, _, need, n_saved), state = _ssm_check(q, k, v, dt, A, D, lengths)
     _need("dy", dy, v.shape, v.dtype, dev)
-    _may("dS_end", dS_end, state, f32, dev)
-    with _on(dev, stream):
-        need = _bytes(e2ttt_ssm_workspace_bytes(shape, 1))
-        _need("saved", saved, (e2ttt_ssm_saved_bytes(shape) // 4,), f32, dev)
-        g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-                 ddt=torch.empty_like(dt), dA=torch.empty_like(A),
-                 dD=None if D is None else torch.empty_like(D),
-                 dS0=torch.empty(state, dtype=f32, device=dev))
-        e2ttt_ssm_scan_bwd(shape, q, k, v, dt, A, D, lengths, saved, dy, dS_end, g["dq"], g["dk"],
-                           g["dv"], g["ddt"], g["dA"], g["dD"], g["dS0"], _scratch(ws, need, dev))
-    return g
+    _need("saved", saved, (n_saved // 4,), torch.float32, dev)
+    if dS_end is not None:
+        _need("dS_end", dS_end, state, torch.float32, dev)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return ssm_scan_bwd(q, k, v, dt, A, saved, dy, D, dS_end, lengths, ws=ws)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ddt, dA = torch.empty_like(dt), torch.empty_like(A)
+    dD = None if D is None else torch.empty_like(D)
+    dS0 = dt.new_empty(state)
+    wp, wn, _keep = _scratch(ws, need, v)
+    _run(_lib.e2ttt_ssm_scan_bwd, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(),
+         A.data_ptr(), _p(D), _p(lengths), saved.data_ptr(), dy.data_ptr(), _p(dS_end), dq.data_ptr(),
+         dk.data_ptr(), dv.data_ptr(), ddt.data_ptr(), dA.data_ptr(), _p(dD), dS0.data_ptr(), wp, wn,
+         _raw_stream(dev))
+    return dict(dq=dq, dk=dk, dv=dv, ddt=ddt, dA=dA, dD=dD, dS0=dS0)
 
 
 def ssm_step(q, k, v, dt, S, A, D=None, *, out=None, stream=None):
     """One token per row: q, k [B, G, d_k], v [B, H, d_v], dt [B, H], S
     [B, H, d_v, d_k] fp32 updated in place. Returns y [B, H, d_v] (`out` where
     given)."""
-    _first("v", v, 3)
+    dev, act = _first("v", v, 3)
+    _dims("q", q, 3, "[B, G, d_k]")
     B, H, d_v = v.shape
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        _refuse("q must be [B, G, d_k]")
-    G, d_k = q.shape[1:]
-    dev, f32 = v.device, torch.float32
-    _need("v", v, v.shape, v.dtype, dev)
-    _need("q", q, (B, G, d_k), v.dtype, dev)
-    _need("k", k, (B, G, d_k), v.dtype, dev)
+    G, d_k = q.shape[1], q.shape[2]
+    f32, qk = torch.float32, (B, G, d_k)
+    _need("q", q, qk, v.dtype, dev)
+    _need("k", k, qk, v.dtype, dev)
     _need("dt", dt, (B, H), f32, dev)
     _need("A", A, (H,), f32, dev)
-    _may("D", D, (H,), f32, dev)
+    if D is not None:
+        _need("D", D, (H,), f32, dev)
     _need("S", S, (B, H, d_v, d_k), f32, dev)
-    _may("out", out, v.shape, v.dtype, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty_like(v)
-        e2ttt_ssm_step(e2ttt_ssm_shape(B, H, G, 1, d_k, d_v, _ACT[v.dtype]), q, k, v, dt, A, D, S, out)
+    if out is not None:
+        _need("out", out, v.shape, v.dtype, dev)
+    shape = _known(_ssm_shape, B, H, G, 1, d_k, d_v, act)[0]
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return ssm_step(q, k, v, dt, S, A, D, out=out)
+    if out is None:
+        out = torch.empty_like(v)
+    _run(_lib.e2ttt_ssm_step, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(),
+         A.data_ptr(), _p(D), S.data_ptr(), out.data_ptr(), _raw_stream(dev))
     return out
 
 
 # ---------------------------------------------------------------- gradient norm
 def _grad_lists(tensors, name):
-    """Pointers, counts, types and device of contiguous CUDA tensors on one device."""
+    """Pointers, counts and types (host arrays) and device number of contiguous
+    CUDA tensors on one device."""
     T = torch.Tensor
     try:
-        act = [_ACT[t.dtype] for t in tensors]
+        act = array("i", [_ACT[t.dtype] for t in tensors])
         devs = set(map(T.get_device, tensors))
         fine = len(devs) == 1 and -1 not in devs and all(map(T.is_contiguous, tensors))
     except (KeyError, AttributeError, TypeError):
         fine = False
     if not fine:
         _refuse(f"{name} must be contiguous bfloat16 or float32 tensors on one CUDA device")
-    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), act, tensors[0].device
+    return array("Q", map(T.data_ptr, tensors)), array("Q", map(T.numel, tensors)), act, devs.pop()
+
+
+def _at(a):
+    return None if a is None else a.buffer_info()[0]
 
 
 def grad_norm(grads, *, ws=None, stream=None):
@@ -418,9 +474,12 @@ def grad_norm(grads, *, ws=None, stream=None):
     if not grads:
         _refuse("grads must not be empty")
     g, n, act, dev = _grad_lists(grads, "grads")
-    with _on(dev, stream):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        e2ttt_grad_norm(g, n, act, norm, _scratch(ws, e2ttt_grad_workspace_bytes(len(g)), dev))
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return grad_norm(grads, ws=ws)
+    norm = grads[0].new_empty((), dtype=torch.float32)
+    wp, wn, _keep = _scratch(ws, e2ttt_grad_workspace_bytes(len(g)), norm)
+    _run(_lib.e2ttt_grad_norm, _at(g), _at(n), _at(act), len(g), norm.data_ptr(), wp, wn, _raw_stream(dev))
     return norm
 
 
@@ -440,8 +499,11 @@ def clip_grad_norm(grads, max_norm, *, out=None, ws=None, stream=None):
         o, on, oact, odev = _grad_lists(out, "out")
         if on != n or oact != act or odev != dev:
             _refuse("out must have the types, sizes and device of grads")
-    with _on(dev, stream):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        e2ttt_clip_grad_norm(g, o, n, act, max_norm, norm,
-                             _scratch(ws, e2ttt_grad_workspace_bytes(len(g)), dev))
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return clip_grad_norm(grads, max_norm, out=out, ws=ws)
+    norm = grads[0].new_empty((), dtype=torch.float32)
+    wp, wn, _keep = _scratch(ws, e2ttt_grad_workspace_bytes(len(g)), norm)
+    _run(_lib.e2ttt_clip_grad_norm, _at(g), _at(o), _at(n), _at(act), len(g), max_norm, norm.data_ptr(),
+         wp, wn, _raw_stream(dev))
     return norm

@@ -146,6 +146,7 @@ __device__ __forceinline__ void decay_add(float& run, float d, float own) { run 
 __device__ __forceinline__ void decay_add(float4& run, float d, const float4& own) {
   run = float4{fmaf(d, run.x, own.x), fmaf(d, run.y, own.y), fmaf(d, run.z, own.z), fmaf(d, run.w, own.w)};
 }
+constexpr int kCarryBatch = 8;  // chunks whose loads are in flight together
 template <typename V, int REV>
 __global__ void __launch_bounds__(kT)
     carry_kernel(int NC, int BH, long long PN, const V* __restrict__ first,
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kT)
   griddep_launch_dependents();
   if (i >= PN) return;
   V run = first ? first[bh * PN + i] : V{};
-  constexpr int U = 8;
+  constexpr int U = kCarryBatch;
   for (int c0 = 0; c0 < NC; c0 += U) {
     V own[U];
     float d[U];
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kT)
     for (int u = 0; u < U; ++u) {
       const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
       if (c0 + u < NC) {
-        own[u] = states[((long long)c * BH + bh) * PN + i];
+        own[u] = __ldcs(states + ((long long)c * BH + bh) * PN + i);
         d[u] = decay[(long long)c * BH + bh];
       }
     }
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kT)
       const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
       if (c0 + u < NC) {
         const long long at = ((long long)c * BH + bh) * PN + i;
-        if (keep) states[at] = run;
+        if (keep) __stcs(states + at, run);
         if (copy) store_bf16(copy + at * W, run);
         decay_add(run, d[u], own[u]);
       }
@@ -456,50 +457,84 @@ __global__ void __launch_bounds__(kT)
   }
 }
 
-// out[b][g][i] = sum over the group's heads and their tiles of part, in order.
-template <typename T>
-__global__ void __launch_bounds__(kT)
-    group_sum_kernel(const float* __restrict__ part, int per, long long row, T* __restrict__ out) {
-  const long long i = (long long)blockIdx.x * kT + threadIdx.x;
+// out[b][g][i] = sum over the group's parts, in order: dq (blockIdx.z 0) and dk
+// (1), V values at a time; the blocks of blockIdx.z 2 take dA and dD.
+template <typename T, int V>
+__device__ __forceinline__ void group_sum(const float* part, int parts, long long row, T* out) {
+  const long long i = ((long long)blockIdx.x * kT + threadIdx.x) * V;
   if (i >= row) return;
-  const float* p = part + (long long)blockIdx.y * per * row + i;
-  float a = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < per; ++j) a += p[(long long)j * row];
-  out[(long long)blockIdx.y * row + i] = from_f<T>(a);
+  const float* p = part + (long long)blockIdx.y * parts * row + i;
+  float a[V] = {};
+#pragma unroll 8
+  for (int j = 0; j < parts; ++j) {
+    float x[V];
+    if constexpr (V == 4) {
+      const float4 f = __ldcs(reinterpret_cast<const float4*>(p));
+      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+    } else {
+      x[0] = *p;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) a[e] += x[e];
+    p += row;
+  }
+  T* o = out + (long long)blockIdx.y * row + i;
+  if constexpr (V == 4 && sizeof(T) == 2) {
+    store_bf16(reinterpret_cast<bf16*>(o), float4{a[0], a[1], a[2], a[3]});
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<float4*>(o) = float4{a[0], a[1], a[2], a[3]};
+  } else {
+    *o = from_f<T>(a[0]);
+  }
+}
+// dA[h], dD[h]: sums of part [rows][H], one block per head, in a fixed order.
+__device__ void head_sum(const float* dAp, const float* dDp, int rows, int H, int h, float* dA, float* dD) {
+  __shared__ double s[2][kT / 32];
+  double a[2] = {0.0, 0.0};
+  for (int i = threadIdx.x; i < rows; i += kT) {
+    a[0] += dAp[(long long)i * H + h];
+    a[1] += dDp[(long long)i * H + h];
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) a[w] += __shfl_xor_sync(~0u, a[w], o);
+    if ((threadIdx.x & 31) == 0) s[w][threadIdx.x >> 5] = a[w];
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    double sum = 0.0;
+    for (int i = 0; i < kT / 32; ++i) sum += s[threadIdx.x][i];
+    float* out = threadIdx.x ? dD : dA;
+    if (out) out[h] = (float)sum;
+  }
+}
+// blockIdx.z: 0 and 1 dq and dk, 2 the heads' sums (blockIdx.z starts at 2 where
+// dq and dk are there already).
+template <typename T, int V>
+__global__ void __launch_bounds__(kT)
+    grad_sums_kernel(const float* __restrict__ dqp, const float* __restrict__ dkp, int parts,
+                     long long row, T* __restrict__ dq, T* __restrict__ dk,
+                     const float* __restrict__ dAp, const float* __restrict__ dDp, int rows, int H,
+                     float* __restrict__ dA, float* __restrict__ dD, int z0) {
+  griddep_wait();
+  const int z = blockIdx.z + z0;
+  if (z == 0) return group_sum<T, V>(dqp, parts, row, dq);
+  if (z == 1) return group_sum<T, V>(dkp, parts, row, dk);
+  for (int h = blockIdx.y * gridDim.x + blockIdx.x; h < H; h += gridDim.x * gridDim.y) {
+    head_sum(dAp, dDp, rows, H, h, dA, dD);
+    __syncthreads();
+  }
 }
 
 __global__ void __launch_bounds__(kT) tile_sum_kernel(const float* __restrict__ part, int tiles,
                                                       long long n, float* __restrict__ out) {
   const long long i = (long long)blockIdx.x * kT + threadIdx.x;
+  griddep_wait();
   if (i >= n) return;
   float a = 0.f;
   for (int j = 0; j < tiles; ++j) a += part[(long long)j * n + i];
   out[i] = a;
-}
-
-// dA[h], dD[h]: sums of part [rows][B][H], one block per head, in a fixed order.
-__global__ void __launch_bounds__(kT) head_sum_kernel(const float* __restrict__ dAp,
-                                                      const float* __restrict__ dDp, int rows, int H,
-                                                      float* __restrict__ dA,
-                                                      float* __restrict__ dD) {
-  __shared__ double s[kT];
-  const int h = blockIdx.x;
-  for (int which = 0; which < 2; ++which) {
-    const float* p = which ? dDp : dAp;
-    float* out = which ? dD : dA;
-    if (!out) continue;
-    double a = 0.0;
-    for (int i = threadIdx.x; i < rows; i += kT) a += p[(long long)i * H + h];
-    s[threadIdx.x] = a;
-    __syncthreads();
-    for (int o = kT / 2; o; o >>= 1) {
-      if (threadIdx.x < o) s[threadIdx.x] += s[threadIdx.x + o];
-      __syncthreads();
-    }
-    if (threadIdx.x == 0) out[h] = (float)s[0];
-    __syncthreads();
-  }
 }
 
 // One token: S = e^{dt A} S + dt v k^T in place, y = S q + D v. Bound by HBM: S
@@ -697,29 +732,29 @@ cudaError_t ssm_carry(const SsmDims& s, bool back, const float* first, const flo
                     first, decay, states, last, (bf16*)copy, keep);
 }
 
+template <typename T>
+static cudaError_t grad_sums_t(const SsmBwdArgs& a, const SsmBwdScratch& w, int parts) {
+  const SsmDims& s = a.s;
+  const long long row = (long long)s.T * s.N;
+  const bool vec = s.N % 4 == 0 && !(((uintptr_t)a.dq | (uintptr_t)a.dk) & (4 * sizeof(T) - 1));
+  const bool direct = s.tc && parts == 1;  // dq and dk are there
+  const long long per = kT * (vec ? 4 : 1);
+  const dim3 grid = direct ? dim3(s.H, 1, 1) : dim3((unsigned)((row + per - 1) / per), s.B * s.G, 3);
+  E2TTT_TRACE("ssm_grad_sums", a.st);
+  return launch_pdl(vec ? grad_sums_kernel<T, 4> : grad_sums_kernel<T, 1>, grid, dim3(kT), 0, a.st,
+                    (const float*)w.dq, (const float*)w.dk, parts, row, (T*)a.dq, (T*)a.dk, (const float*)w.dA,
+                    (const float*)w.dD, s.NC * s.NPT * s.B, s.H, a.dA, a.dD, direct ? 2 : 0);
+}
 cudaError_t ssm_grad_sums(const SsmBwdArgs& a, const SsmBwdScratch& w, int parts) {
   const SsmDims& s = a.s;
-  cudaError_t e;
-  const long long row = (long long)s.T * s.N, n = (long long)s.B * s.H * s.T;
-  const dim3 grid((unsigned)((row + kT - 1) / kT), s.B * s.G);
-  if (!s.tc || parts > 1) {
-    E2TTT_TRACE("ssm_group_sum", a.st);
-    for (int i = 0; i < 2; ++i) {
-      if (s.bf16_act)
-        group_sum_kernel<bf16><<<grid, kT, 0, a.st>>>(i ? w.dk : w.dq, parts, row, (bf16*)(i ? a.dk : a.dq));
-      else
-        group_sum_kernel<float><<<grid, kT, 0, a.st>>>(i ? w.dk : w.dq, parts, row, (float*)(i ? a.dk : a.dq));
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-  }
   if (s.NPT > 1) {
+    const long long n = (long long)s.B * s.H * s.T;
     E2TTT_TRACE("ssm_tile_sum", a.st);
-    tile_sum_kernel<<<(unsigned)((n + kT - 1) / kT), kT, 0, a.st>>>(w.ddt, s.NPT, n, a.ddt);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const cudaError_t e = launch_pdl(tile_sum_kernel, dim3((unsigned)((n + kT - 1) / kT)), dim3(kT), 0, a.st,
+                                     (const float*)w.ddt, s.NPT, n, a.ddt);
+    if (e != cudaSuccess) return e;
   }
-  E2TTT_TRACE("ssm_head_sum", a.st);
-  head_sum_kernel<<<s.H, kT, 0, a.st>>>(w.dA, w.dD, s.NC * s.NPT * s.B, s.H, a.dA, a.dD);
-  return cudaGetLastError();
+  return s.bf16_act ? grad_sums_t<bf16>(a, w, parts) : grad_sums_t<float>(a, w, parts);
 }
 
 size_t ssm_bwd_workspace_bytes(const SsmDims& s) {

@@ -1,11 +1,7 @@
-// State-space scan, fp32 CUDA-core kernels for every size and type, and the
-// passes over chunk states that all forms share. The mathematics is in ssm.cuh.
+// State-space scan in fp32 for every size and type, and the passes over chunk states that all forms share. The mathematics is in ssm.cuh.
 //
-// A chunk's work is a handful of small matrix products, done here from shared
-// memory by 16 x 16 threads with 4 x 4 results each; chunks meet only in their
-// states, which one elementwise pass carries along the tokens.
-#include <type_traits>
-
+// A chunk's work is a handful of small matrix products from shared memory; chunks
+// meet only in their states, which one elementwise pass carries along the tokens.
 #include "ssm.cuh"
 #include "trace.h"
 
@@ -14,39 +10,76 @@ namespace {
 
 constexpr int kT = 256;
 
-// acc[i][j] += sum_k A(m_i, k) B(k, n_j), m_i = ty + 16 i, n_j = n0 + tx + 16 j
-// clamped to nmax. A at a + m*am + k*ak, B at b + k*bk + n*bn.
+// Products of fp32 tiles in shared memory on the warps' tensor instructions
+// (m16n8k8, tf32): each operand enters as two tf32 terms, a = a0 + a1 to 22 bits,
+// and a b = a0 b0 + a0 b1 + a1 b0 (what is left out is 2^-22 of it). Against plain
+// fp32 multiply-adds from shared memory this reads each operand value once per 16
+// or 8 results instead of once per 4.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// The block's 8 warps share a result of R * 16 rows x 64 columns: R warps down, W
+// = 8 / R across, each 16 rows by R * 8 columns. Result e of column tile j of a
+// thread is at row() + 8 (e >> 1), col(j) + (e & 1).
 template <int R>
-__device__ __forceinline__ void tile_mm(float (&acc)[R][4], const float* a, int am, int ak,
-                                        const float* b, int bk, int bn, int K, int n0, int nmax) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int no[4];
+struct Tile {
+  static constexpr int W = 8 / R;
+  float v[R][4];
+  static __device__ __forceinline__ int row() { return (threadIdx.x >> 5) % R * 16 + (threadIdx.x & 31) / 4; }
+  static __device__ __forceinline__ int across() { return (threadIdx.x >> 5) / R; }
+  static __device__ __forceinline__ int col(int j) { return across() * R * 8 + j * 8 + (threadIdx.x & 3) * 2; }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) no[j] = min(n0 + tx + 16 * j, nmax) * bn;
-  for (int k = 0; k < K; ++k) {
-    float x[R], y[4];
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int i = 0; i < R; ++i) x[i] = a[(ty + 16 * i) * am + k * ak];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = b[k * bk + no[j]];
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+      for (int e = 0; e < 4; ++e) v[j][e] = 0.f;
   }
-}
-template <int R>
-__device__ __forceinline__ void clear(float (&acc)[R][4]) {
+  // += sum_k A(m, k) B(k, n0 + n): A at a + m*am + k*ak, B at b + k*bk + n*bn, for
+  // K a multiple of 8 (zeros where the data ends) and columns up to nmax (clamped).
+  __device__ __forceinline__ void mm(const float* a, int am, int ak, const float* b, int bk, int bn, int K,
+                                     int n0, int nmax) {
+    const int q = threadIdx.x & 3, r = (threadIdx.x & 31) / 4;
+    const float* a0 = a + row() * am + q * ak;
+    const float* b0[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+    for (int j = 0; j < R; ++j) b0[j] = b + min(n0 + across() * R * 8 + j * 8 + r, nmax) * bn + q * bk;
+#pragma unroll 2
+    for (int k = 0; k < K; k += 8) {
+      uint32_t ah[4], al[4];
+      split_tf32(a0[k * ak], ah[0], al[0]);
+      split_tf32(a0[k * ak + 8 * am], ah[1], al[1]);
+      split_tf32(a0[(k + 4) * ak], ah[2], al[2]);
+      split_tf32(a0[(k + 4) * ak + 8 * am], ah[3], al[3]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-}
-// Sum over the 16 threads that share ty.
-__device__ __forceinline__ float row_sum16(float x) {
+      for (int j = 0; j < R; ++j) {
+        uint32_t bh[2], bl[2];
+        split_tf32(b0[j][k * bk], bh[0], bl[0]);
+        split_tf32(b0[j][(k + 4) * bk], bh[1], bl[1]);
+        // Eight products at a time from zero, then added with rounding: the tensor
+        // instructions' own additions cut off, which over a long sum would lean one way.
+        float t[4] = {};
+        mma_tf32(t, al, bh);
+        mma_tf32(t, ah, bl);
+        mma_tf32(t, ah, bh);
 #pragma unroll
-  for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  return x;
+        for (int e = 0; e < 4; ++e) v[j][e] += t[e];
+      }
+    }
+  }
+};
+// Sum over the four threads that share a row.
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(~0u, x, 1);
+  return x + __shfl_xor_sync(~0u, x, 2);
 }
 
 // rows x cols of src (row pitch `ld`) to dst (row pitch `pitch`), as fp32; rows
@@ -59,6 +92,12 @@ __device__ __forceinline__ void load_tile(float* dst, int pitch, const T* src, l
     dst[r * pitch + c] = r < n && c < cols ? to_f<T>(src[(long long)r * ld + c]) : 0.f;
   }
 }
+
+// State columns as the products contract them: a multiple of 8, zeros beyond N. A
+// row's pitch is 4 more, so that the 8 rows and 4 columns that a warp reads at
+// once fall into 32 different banks.
+__host__ __device__ __forceinline__ int pad8(int n) { return (n + 7) & ~7; }
+constexpr int kXP = kSsmPT + 4;
 
 struct Where {
   int b, h, g, pt, c, bh, t0, n, p0, np;
@@ -100,12 +139,12 @@ __global__ void __launch_bounds__(kT)
   extern __shared__ float sm[];
   const Where w = where(s, lengths);
   if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0) *status = 0;  // nothing here waits
-  const int Q = s.Q, N = s.N, XP = kSsmPT + 1, NP = N + 1;
+  const int Q = s.Q, N = s.N, XP = kXP, NP = pad8(N) + 4;
   const ChunkLogs L = chunk_logs(sm, Q);
   float* xs = sm + 3 * Q;
   float* ys = xs + Q * XP;
   if (threadIdx.x < 32) fill_chunk_logs(L, dt + (long long)w.bh * s.T + w.t0, A[w.h], w.n);
-  load_tile<T>(ys, NP, y + (((long long)w.b * s.G + w.g) * s.T + w.t0) * N, N, Q, w.n, N, N);
+  load_tile<T>(ys, NP, y + (((long long)w.b * s.G + w.g) * s.T + w.t0) * N, N, Q, w.n, N, pad8(N));
   load_tile<T>(xs, XP, x + ((long long)w.bh * s.T + w.t0) * s.P + w.p0, s.P, Q, w.n, w.np, kSsmPT);
   __syncthreads();
   for (int i = threadIdx.x; i < Q * kSsmPT; i += kT) {
@@ -116,17 +155,16 @@ __global__ void __launch_bounds__(kT)
     decay[(long long)w.c * s.B * s.H + w.bh] = L.from_start(Q - 1);
   __syncthreads();
   float* out = states + (((long long)w.c * s.B * s.H + w.bh) * s.P + w.p0) * N;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   for (int n0 = 0; n0 < N; n0 += 64) {
-    float acc[4][4];
-    clear(acc);
-    tile_mm<4>(acc, xs, 1, XP, ys, NP, 1, Q, n0, N - 1);
+    Tile<4> acc;
+    acc.clear();
+    acc.mm(xs, 1, XP, ys, NP, 1, Q, n0, N - 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int p = ty + 16 * i, n = n0 + tx + 16 * j;
-        if (p < w.np && n < N) out[(long long)p * N + n] = acc[i][j];
+      for (int e = 0; e < 4; ++e) {
+        const int p = acc.row() + 8 * (e >> 1), n = n0 + acc.col(j) + (e & 1);
+        if (p < w.np && n < N) out[(long long)p * N + n] = acc.v[j][e];
       }
   }
 }
@@ -195,7 +233,7 @@ __global__ void __launch_bounds__(kT)
                      T* __restrict__ y) {
   extern __shared__ float sm[];
   const Where w = where(s, lengths);
-  const int Q = s.Q, N = s.N, XP = kSsmPT + 1, NP = N + 1, QP = Q + 1;
+  const int Q = s.Q, N = s.N, XP = kXP, NP = pad8(N) + 4, QP = Q + 4;
   const ChunkLogs L = chunk_logs(sm, Q);
   float* qs = sm + 3 * Q;
   float* ks = qs + Q * NP;  // then the state [PT][NP]
@@ -203,44 +241,42 @@ __global__ void __launch_bounds__(kT)
   float* ws = xs + Q * XP;
   if (threadIdx.x < 32) fill_chunk_logs(L, dt + (long long)w.bh * s.T + w.t0, A[w.h], w.n);
   const long long qo = (((long long)w.b * s.G + w.g) * s.T + w.t0) * N;
-  load_tile<T>(qs, NP, q + qo, N, Q, w.n, N, N);
-  load_tile<T>(ks, NP, k + qo, N, Q, w.n, N, N);
+  load_tile<T>(qs, NP, q + qo, N, Q, w.n, N, pad8(N));
+  load_tile<T>(ks, NP, k + qo, N, Q, w.n, N, pad8(N));
   load_tile<T>(xs, XP, v + ((long long)w.bh * s.T + w.t0) * s.P + w.p0, s.P, Q, w.n, w.np, kSsmPT);
   __syncthreads();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[R][4];
-  clear(acc);
-  tile_mm<R>(acc, qs, NP, 1, ks, 1, NP, N, 0, Q - 1);
+  const int NK = pad8(N);
+  Tile<R> acc;
+  acc.clear();
+  acc.mm(qs, NP, 1, ks, 1, NP, NK, 0, Q - 1);
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = ty + 16 * i, u = tx + 16 * j;
-      if (u < Q) ws[t * QP + u] = u <= t ? acc[i][j] * L.decay(t, u) * L.eta[u] : 0.f;
+    for (int e = 0; e < 4; ++e) {
+      const int t = acc.row() + 8 * (e >> 1), u = acc.col(j) + (e & 1);
+      const float x = acc.v[j][e] * (L.decay(t, min(u, Q - 1)) * L.eta[min(u, Q - 1)]);
+      if (u < Q) ws[t * QP + u] = u <= t ? x : 0.f;
     }
   __syncthreads();
   load_tile<float>(ks, NP, states + (((long long)w.c * s.B * s.H + w.bh) * s.P + w.p0) * N, N, kSsmPT,
-                   w.np, N, N);
+                   w.np, N, NK);
   __syncthreads();
-  clear(acc);
-  tile_mm<R>(acc, qs, NP, 1, ks, 1, NP, N, 0, kSsmPT - 1);
+  acc.clear();
+  acc.mm(qs, NP, 1, ks, 1, NP, NK, 0, kSsmPT - 1);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const float f = L.from_start(ty + 16 * i);
+  for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] *= f;
-  }
-  tile_mm<R>(acc, ws, QP, 1, xs, XP, 1, Q, 0, kSsmPT - 1);
+    for (int e = 0; e < 4; ++e) acc.v[j][e] *= L.from_start(acc.row() + 8 * (e >> 1));
+  acc.mm(ws, QP, 1, xs, XP, 1, Q, 0, kSsmPT - 1);
   const float Dh = D ? D[w.h] : 0.f;
   T* out = y + ((long long)w.bh * s.T + w.t0) * s.P + w.p0;
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = ty + 16 * i, p = tx + 16 * j;
-      if (w.t0 + t < s.T && p < w.np)
-        out[(long long)t * s.P + p] =
-            from_f<T>(t < w.n ? fmaf(Dh, xs[t * XP + p], acc[i][j]) : 0.f);
+    for (int e = 0; e < 4; ++e) {
+      const int t = acc.row() + 8 * (e >> 1), p = acc.col(j) + (e & 1);
+      const float o = fmaf(Dh, xs[t * XP + min(p, kSsmPT - 1)], acc.v[j][e]);
+      if (w.t0 + t < s.T && p < w.np) out[(long long)t * s.P + p] = from_f<T>(t < w.n ? o : 0.f);
     }
 }
 
@@ -272,10 +308,12 @@ __global__ void __launch_bounds__(kT)
                       float* __restrict__ ddtp, float* __restrict__ dAp, float* __restrict__ dDp) {
   extern __shared__ float sm[];
   const Where w = where(s, lengths);
-  const int Q = s.Q, N = s.N, XP = kSsmPT + 1, NP = N + 1, QP = Q + 1;
+  const int Q = s.Q, N = s.N, XP = kXP, NP = pad8(N) + 4, QP = Q + 4;
   const ChunkLogs L = chunk_logs(sm, Q);
-  float* dots = sm + 3 * Q;  // [6][Q]: row sums, column sums, readers', sources', deta, K's diagonal
-  float* scratch = dots + 6 * Q;
+  // [4][Q]: row sums of Z off its diagonal, column sums of Z / eta off it, and the
+  // diagonals of Z / eta and of K
+  float* dots = sm + 3 * Q;
+  float* scratch = dots + 4 * Q;
   float* qs = scratch + 16;
   float* ks = qs + Q * NP;
   float* Ss = ks + Q * NP;
@@ -284,148 +322,132 @@ __global__ void __launch_bounds__(kT)
   float* gs = xs + Q * XP;
   float* Ws = gs + Q * XP;  // e^{c_t-c_s} (q_t.k_s)
   float* Ks = Ws + Q * QP;  // e^{c_t-c_s} eta_s (dy_t.v_s)
-  float* cz = Ks + Q * QP;  // [2][16][Q]: column sums by thread row, of Z off its diagonal and of deta
+  float* cz = Ks + Q * QP;  // [8][Q]: sums by warp
   if (threadIdx.x < 32) fill_chunk_logs(L, dt + (long long)w.bh * s.T + w.t0, A[w.h], w.n);
   const long long qo = (((long long)w.b * s.G + w.g) * s.T + w.t0) * N;
   const long long vo = ((long long)w.bh * s.T + w.t0) * s.P + w.p0;
   const long long so = (((long long)w.c * s.B * s.H + w.bh) * s.P + w.p0) * N;
-  load_tile<T>(qs, NP, q + qo, N, Q, w.n, N, N);
-  load_tile<T>(ks, NP, k + qo, N, Q, w.n, N, N);
+  load_tile<T>(qs, NP, q + qo, N, Q, w.n, N, pad8(N));
+  load_tile<T>(ks, NP, k + qo, N, Q, w.n, N, pad8(N));
   load_tile<T>(xs, XP, v + vo, s.P, Q, w.n, w.np, kSsmPT);
   load_tile<T>(gs, XP, dy + vo, s.P, Q, w.n, w.np, kSsmPT);
-  load_tile<float>(Ss, NP, states + so, N, kSsmPT, w.np, N, N);
-  load_tile<float>(Xs, NP, ends + so, N, kSsmPT, w.np, N, N);
+  load_tile<float>(Ss, NP, states + so, N, kSsmPT, w.np, N, pad8(N));
+  load_tile<float>(Xs, NP, ends + so, N, kSsmPT, w.np, N, pad8(N));
   __syncthreads();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int NK = pad8(N);
   {
-    float m[R][4], kk[R][4];
-    clear(m);
-    clear(kk);
-    tile_mm<R>(m, qs, NP, 1, ks, 1, NP, N, 0, Q - 1);
-    tile_mm<R>(kk, gs, XP, 1, xs, 1, XP, kSsmPT, 0, Q - 1);
-    float colz[4] = {}, cold[4] = {};
+    Tile<R> m, kk;
+    m.clear();
+    kk.clear();
+    m.mm(qs, NP, 1, ks, 1, NP, NK, 0, Q - 1);
+    kk.mm(gs, XP, 1, xs, 1, XP, kSsmPT, 0, Q - 1);
+    float rows[2] = {};
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int t = ty + 16 * i;
-      float rows = 0.f;
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int u = tx + 16 * j;
-        if (u >= Q) continue;
-        const float e = u <= t ? L.decay(t, u) : 0.f;
-        const float a = u <= t ? e * m[i][j] : 0.f;
-        const float b = u <= t ? e * L.eta[u] * kk[i][j] : 0.f;
-        Ws[t * QP + u] = a;
-        Ks[t * QP + u] = b;
-        const float r = a * kk[i][j], z = u < t ? r * L.eta[u] : 0.f;
-        rows += z;
-        colz[j] += z;
-        cold[j] += r;
-        if (u == t) dots[5 * Q + t] = kk[i][j];
+      for (int e = 0; e < 4; ++e) {
+        const int t = m.row() + 8 * (e >> 1), u = m.col(j) + (e & 1), uc = min(u, Q - 1);
+        const float d = L.decay(t, uc), eta = L.eta[uc];
+        const float a = u <= t ? d * m.v[j][e] : 0.f;
+        const float r = u <= t ? a * kk.v[j][e] : 0.f;
+        if (u < Q) {
+          Ws[t * QP + u] = a;
+          Ks[t * QP + u] = u <= t ? d * eta * kk.v[j][e] : 0.f;
+          if (u == t) {
+            dots[3 * Q + t] = kk.v[j][e];
+            dots[2 * Q + t] = r;
+          }
+        }
+        m.v[j][e] = u < t && u < Q ? r : 0.f;  // Z / eta off the diagonal
+        rows[e >> 1] = fmaf(m.v[j][e], eta, rows[e >> 1]);
       }
-      rows = row_sum16(rows);
-      if (tx == 0) dots[t] = rows;
-    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int u = tx + 16 * j;
-      if (u >= Q) continue;
-      cz[ty * Q + u] = colz[j];
-      cz[(16 + ty) * Q + u] = cold[j];
+    for (int i = 0; i < 2; ++i) {
+      rows[i] = quad_sum(rows[i]);
+      if ((threadIdx.x & 3) == 0) cz[m.across() * Q + m.row() + 8 * i] = rows[i];
     }
+    // column sums: over the 8 rows that a thread's column has in the warp, twice
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float c = m.v[j][e] + m.v[j][e + 2];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) c += __shfl_xor_sync(~0u, c, o);
+        const int u = m.col(j) + e;
+        if ((threadIdx.x & 31) < 4 && u < Q) cz[(4 + (threadIdx.x >> 5) % R) * Q + u] = c;
+      }
   }
   __syncthreads();
   for (int u = threadIdx.x; u < Q; u += kT) {
-    float z = 0.f, de = 0.f;
-    for (int i = 0; i < 16; ++i) {
-      z += cz[i * Q + u];
-      de += cz[(16 + i) * Q + u];
-    }
-    dots[Q + u] = z;
-    dots[4 * Q + u] = de;
+    float z = 0.f, c = 0.f;
+    for (int i = 0; i < Tile<R>::W; ++i) z += cz[i * Q + u];
+    for (int i = 0; i < R; ++i) c += cz[(4 + i) * Q + u];
+    dots[u] = z;
+    dots[Q + u] = c;
   }
   // dv
   {
-    float acc[R][4];
-    clear(acc);
-    tile_mm<R>(acc, ks, NP, 1, Xs, 1, NP, N, 0, kSsmPT - 1);
+    Tile<R> acc;
+    acc.clear();
+    acc.mm(ks, NP, 1, Xs, 1, NP, NK, 0, kSsmPT - 1);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const float f = L.to_end(ty + 16 * i);
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] *= f;
-    }
-    tile_mm<R>(acc, Ws, 1, QP, gs, XP, 1, Q, 0, kSsmPT - 1);
+      for (int e = 0; e < 4; ++e) acc.v[j][e] *= L.to_end(acc.row() + 8 * (e >> 1));
+    acc.mm(Ws, 1, QP, gs, XP, 1, Q, 0, kSsmPT - 1);
     const float Dh = D ? D[w.h] : 0.f;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = ty + 16 * i, p = tx + 16 * j;
-        if (w.t0 + t < s.T && p < w.np)
-          dv[vo + (long long)t * s.P + p] =
-              from_f<T>(t < w.n ? fmaf(L.eta[t], acc[i][j], Dh * gs[t * XP + p]) : 0.f);
+      for (int e = 0; e < 4; ++e) {
+        const int t = acc.row() + 8 * (e >> 1), p = acc.col(j) + (e & 1);
+        const float o = fmaf(L.eta[t], acc.v[j][e], Dh * gs[t * XP + min(p, kSsmPT - 1)]);
+        if (w.t0 + t < s.T && p < w.np) dv[vo + (long long)t * s.P + p] = from_f<T>(t < w.n ? o : 0.f);
       }
   }
   // dq, dk and the dots of their state parts
   const long long po = (((long long)w.bh * s.NPT + w.pt) * s.T + w.t0) * N;
-  float rd[R], sd[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) rd[i] = sd[i] = 0.f;
+  float dot[2][2] = {};  // of dq, dk; of this thread's two rows
   for (int n0 = 0; n0 < N; n0 += 64) {
-    float acc[R][4];
-    clear(acc);
-    tile_mm<R>(acc, gs, XP, 1, Ss, NP, 1, kSsmPT, n0, N - 1);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int t = ty + 16 * i;
-      const float f = L.from_start(t);
+    for (int which = 0; which < 2; ++which) {
+      const float* mine = which ? ks : qs;
+      float* out = which ? dkp : dqp;
+      Tile<R> acc;
+      acc.clear();
+      acc.mm(which ? xs : gs, XP, 1, which ? Xs : Ss, NP, 1, kSsmPT, n0, N - 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx + 16 * j;
-        acc[i][j] *= f;
-        if (n < N) rd[i] = fmaf(acc[i][j], qs[t * NP + n], rd[i]);
-      }
-    }
-    tile_mm<R>(acc, Ks, QP, 1, ks, NP, 1, Q, n0, N - 1);
+      for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+        for (int e = 0; e < 4; ++e) {
+          const int t = acc.row() + 8 * (e >> 1), n = n0 + acc.col(j) + (e & 1);
+          const float x = acc.v[j][e] * (which ? L.to_end(t) : L.from_start(t));
+          dot[which][e >> 1] = fmaf(n < N ? x : 0.f, mine[t * NP + min(n, N - 1)], dot[which][e >> 1]);
+          acc.v[j][e] = which ? x * L.eta[t] : x;
+        }
+      if (which)
+        acc.mm(Ks, 1, QP, qs, NP, 1, Q, n0, N - 1);
+      else
+        acc.mm(Ks, QP, 1, ks, NP, 1, Q, n0, N - 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = ty + 16 * i, n = n0 + tx + 16 * j;
-        if (w.t0 + t < s.T && n < N) dqp[po + (long long)t * N + n] = t < w.n ? acc[i][j] : 0.f;
-      }
-    clear(acc);
-    tile_mm<R>(acc, xs, XP, 1, Xs, NP, 1, kSsmPT, n0, N - 1);
+      for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int t = ty + 16 * i;
-      const float f = L.to_end(t);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx + 16 * j;
-        acc[i][j] *= f;
-        if (n < N) sd[i] = fmaf(acc[i][j], ks[t * NP + n], sd[i]);
-        acc[i][j] *= L.eta[t];
-      }
-    }
-    tile_mm<R>(acc, Ks, 1, QP, qs, NP, 1, Q, n0, N - 1);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = ty + 16 * i, n = n0 + tx + 16 * j;
-        if (w.t0 + t < s.T && n < N) dkp[po + (long long)t * N + n] = t < w.n ? acc[i][j] : 0.f;
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const float a = row_sum16(rd[i]), b = row_sum16(sd[i]);
-    if (tx == 0) {
-      dots[2 * Q + ty + 16 * i] = a;
-      dots[3 * Q + ty + 16 * i] = b;
+        for (int e = 0; e < 4; ++e) {
+          const int t = acc.row() + 8 * (e >> 1), n = n0 + acc.col(j) + (e & 1);
+          if (w.t0 + t < s.T && n < N) out[po + (long long)t * N + n] = t < w.n ? acc.v[j][e] : 0.f;
+        }
     }
   }
+  __syncthreads();  // the column sums' scratch has been read
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float x = quad_sum(dot[which][i]);
+      if ((threadIdx.x & 3) == 0)
+        cz[(which * 4 + Tile<R>::across()) * Q + Tile<R>::row() + 8 * i] = x;
+    }
   // e^{c_Q} <S, X>
   float ip = 0.f;
   for (int i = threadIdx.x; i < kSsmPT * N; i += kT) {
@@ -433,27 +455,59 @@ __global__ void __launch_bounds__(kT)
     ip = fmaf(Ss[p * NP + n], Xs[p * NP + n], ip);
   }
   ip = block_sum0(ip, scratch);
-  if (threadIdx.x == 0) {
-    const float* rows = dots;
-    const float *cols = dots + Q, *rdr = dots + 2 * Q, *src = dots + 3 * Q, *de = dots + 4 * Q,
-                *kd = dots + 5 * Q;
-    const double through = (double)L.from_start(Q - 1) * ip;
-    double before = 0.0;  // sources before r, read after the chunk
-    for (int r = 0; r < Q; ++r) before += (double)L.eta[r] * src[r];
-    double after = 0.0, dA = 0.0, dD = 0.0;
-    const float Ah = A[w.h];
-    float* out = ddtp + ((long long)w.pt * s.B * s.H + w.bh) * s.T + w.t0;
-    for (int r = Q - 1; r >= 0; --r) {
-      before -= (double)L.eta[r] * src[r];
-      after += (double)rows[r] - cols[r] + rdr[r];
-      const double dl = after + before + through;
-      dA += L.eta[r] * dl;
-      dD += kd[r];
-      if (w.t0 + r < s.T) out[r] = r < w.n ? (float)(Ah * dl + de[r] + src[r]) : 0.f;
+  if (threadIdx.x < 32) {
+    // ddt, dA, dD: lane l has the tokens l * K .. l * K + K - 1
+    constexpr int K = R / 2;  // Q / 32
+    const int lane = threadIdx.x;
+    float a4[K], b4[K], src[K], as = 0.f, bs = 0.f, dD = 0.f;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int r = lane * K + i;
+      float rd = 0.f;
+      src[i] = 0.f;
+      for (int x = 0; x < Tile<R>::W; ++x) {
+        rd += cz[x * Q + r];
+        src[i] += cz[(4 + x) * Q + r];
+      }
+      a4[i] = (dots[r] - L.eta[r] * dots[Q + r]) + rd;
+      b4[i] = L.eta[r] * src[i];
+      as += a4[i];
+      bs += b4[i];
+      dD += dots[3 * Q + r];
     }
-    const long long o = ((long long)w.c * s.NPT + w.pt) * s.B * s.H + w.bh;
-    dAp[o] = (float)dA;
-    dDp[o] = (float)dD;
+    float after = as, before = bs;  // of this lane's tokens on; up to them
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const float x = __shfl_down_sync(~0u, after, d), y = __shfl_up_sync(~0u, before, d);
+      after += lane + d < 32 ? x : 0.f;
+      before += lane >= d ? y : 0.f;
+    }
+    // exclusive of this lane's own, without taking them off again
+    after = __shfl_down_sync(~0u, after, 1);
+    before = __shfl_up_sync(~0u, before, 1);
+    after = lane < 31 ? after : 0.f;
+    before = lane > 0 ? before : 0.f;
+    const float through = L.from_start(Q - 1) * __shfl_sync(~0u, ip, 0), Ah = A[w.h];
+    const double dA = decay_gradient<K>(a4, b4, L.eta + lane * K, through, lane);
+    float dl[K];
+#pragma unroll
+    for (int i = K - 1; i >= 0; --i) dl[i] = after += a4[i];
+    float* out = ddtp + ((long long)w.pt * s.B * s.H + w.bh) * s.T + w.t0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int r = lane * K + i;
+      dl[i] += before + through;
+      before += b4[i];
+      const float x = fmaf(Ah, dl[i], dots[Q + r] + dots[2 * Q + r] + src[i]);
+      if (w.t0 + r < s.T) out[r] = r < w.n ? x : 0.f;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) dD += __shfl_xor_sync(~0u, dD, d);
+    if (lane == 0) {
+      const long long o = ((long long)w.c * s.NPT + w.pt) * s.B * s.H + w.bh;
+      dAp[o] = (float)dA;
+      dDp[o] = dD;
+    }
   }
 }
 
@@ -621,16 +675,16 @@ __global__ void __launch_bounds__(kT)
 }
 
 size_t state_smem(const SsmDims& s) {
-  return sizeof(float) * (3 * s.Q + (size_t)s.Q * (kSsmPT + 1) + (size_t)s.Q * (s.N + 1));
+  return sizeof(float) * (3 * s.Q + (size_t)s.Q * kXP + (size_t)s.Q * (pad8(s.N) + 4));
 }
 size_t out_smem(const SsmDims& s) {
-  return sizeof(float) * (3 * s.Q + (size_t)(s.Q + (s.Q > kSsmPT ? s.Q : kSsmPT)) * (s.N + 1) +
-                          (size_t)s.Q * (kSsmPT + 1) + (size_t)s.Q * (s.Q + 1));
+  return sizeof(float) * (3 * s.Q + (size_t)(s.Q + (s.Q > kSsmPT ? s.Q : kSsmPT)) * (pad8(s.N) + 4) +
+                          (size_t)s.Q * kXP + (size_t)s.Q * (s.Q + 4));
 }
 size_t grad_smem(const SsmDims& s) {
-  return sizeof(float) * (9 * s.Q + 16 + (size_t)2 * (s.Q + kSsmPT) * (s.N + 1) +
-                          (size_t)2 * s.Q * (kSsmPT + 1) + (size_t)2 * s.Q * (s.Q + 1) +
-                          (size_t)32 * s.Q);
+  return sizeof(float) * (7 * s.Q + 16 + (size_t)2 * (s.Q + kSsmPT) * (pad8(s.N) + 4) +
+                          (size_t)2 * s.Q * kXP + (size_t)2 * s.Q * (s.Q + 4) +
+                          (size_t)8 * s.Q);
 }
 
 template <class F>
@@ -679,9 +733,7 @@ cudaError_t fwd_t(const SsmFwdArgs& a) {
   }
   if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, nullptr, true, a.st)) != cudaSuccess) return e;
   E2TTT_TRACE("ssm_chunk_out", a.st);
-  auto kern = chunk_out_kernel<T, 2>;
-  if constexpr (std::is_same<T, float>::value)  // bf16 with so few columns runs on the tensor cores
-    if (s.Q == 64) kern = chunk_out_kernel<T, 4>;
+  auto kern = s.Q == 64 ? chunk_out_kernel<T, 4> : chunk_out_kernel<T, 2>;
   if ((e = allow_smem(kern, out_smem(s))) != cudaSuccess) return e;
   kern<<<grid, kT, out_smem(s), a.st>>>(s, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.dt, a.A,
                                         a.D, a.lengths, a.states, (T*)a.y);
@@ -703,9 +755,7 @@ cudaError_t bwd_t(const SsmBwdArgs& a, const SsmBwdScratch& w) {
   if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, nullptr, true, a.st)) != cudaSuccess) return e;
   {
     E2TTT_TRACE("ssm_chunk_grad", a.st);
-    auto kern = chunk_grad_kernel<T, 2>;
-    if constexpr (std::is_same<T, float>::value)  // bf16 with so few columns runs on the tensor cores
-      if (s.Q == 64) kern = chunk_grad_kernel<T, 4>;
+    auto kern = s.Q == 64 ? chunk_grad_kernel<T, 4> : chunk_grad_kernel<T, 2>;
     if ((e = allow_smem(kern, grad_smem(s))) != cudaSuccess) return e;
     kern<<<grid, kT, grad_smem(s), a.st>>>(s, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.dt, a.A,
                                            a.D, a.lengths, a.states, w.ends, (const T*)a.dy, w.dq, w.dk,

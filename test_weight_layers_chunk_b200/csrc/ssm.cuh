@@ -82,6 +82,33 @@ __device__ __forceinline__ void fill_chunk_logs(const ChunkLogs& L, const float*
   }
 }
 
+// A chunk's part of dA = sum_r eta_r dl_r, by one warp (lane l has the tokens l K ..
+// l K + K - 1), with dl_r = sum_{t>=r} a_t + sum_{s<r} b_s + through. Summed the
+// other way round, with E_t = eta_1 + .. + eta_t, it is
+//   sum_t a_t E_t + sum_s b_s (E_Q - E_s) + through E_Q,
+// in fp64: the chunks' parts cancel to a few hundredths of their size.
+template <int K>
+__device__ __forceinline__ double decay_gradient(const float (&a)[K], const float (&b)[K], const float* eta,
+                                                 float through, int lane) {
+  double E[K], run = 0.0;
+#pragma unroll
+  for (int i = 0; i < K; ++i) E[i] = run += eta[i];
+  double pre = run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double u = __shfl_up_sync(~0u, pre, o);
+    pre += lane >= o ? u : 0.0;
+  }
+  const double all = __shfl_sync(~0u, pre, 31);
+  pre -= run;
+  double sum = lane == 0 ? through * all : 0.0;
+#pragma unroll
+  for (int i = 0; i < K; ++i) sum += a[i] * (pre + E[i]) + b[i] * (all - (pre + E[i]));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  return sum;
+}
+
 __device__ __forceinline__ int ssm_row_length(const int* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }

@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the decay taken exactly within the row's own block of 32 tokens, and as
 // e^{c_t-c_r} e^{c_r-c_s} with r the last token of an earlier block (two factors
 // that are both at most one for a decaying state), so that only a quarter of the
-// decays takes an exponential each.
+// decays takes an exponential each. A token's own term, W_tt v_t, joins D v_t in
+// fp32 instead: where it is most of y_t, y_t then has no rounding but its last.
 template <int NB, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     out_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const bf16* __restrict__ states, bf16* __restrict__ y, int per,
                int* __restrict__ status) {
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(16) float slog[2][3 * kQ], stail[2][kQ];
+  __shared__ __align__(16) float slog[2][3 * kQ], stail[2][kQ], own[kQ];
   __shared__ uint64_t bar, gbar[2];
   __shared__ uint32_t slot;
   const int wg = threadIdx.x / kHalf, t = threadIdx.x % kQ, half = threadIdx.x / kQ & 1, quad = t >> 5;
@@ -539,7 +540,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t kYi = 128 + wg * 128, kYd = kYi + 64;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   if (first.wait()) {
-    // the scores above the diagonal blocks are zero for every item
+    // q_t.k_t; the scores above the diagonal blocks are zero for every item
+    if (wg == 0 && half == 0) {
+      float a[32], x = 0.f;
+      tc::tmem_ld32(lanes + quad * 32, a);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x = t == quad * 32 + i ? a[i] : x;
+      own[t] = x;
+    }
+    __syncthreads();
     for (int cb = half; cb < 4; cb += 2)
       if (cb > quad)
 #pragma unroll
@@ -602,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float w2 = a[i * 4 + 2] * (ex2((thi - uh.z) + (tlo - ul.z)) * ue.z);
           const float w3 = a[i * 4 + 3] * (ex2((thi - uh.w) + (tlo - ul.w)) * ue.w);
           uint32_t* ow = &o[i >> 1].x + (i & 1) * 2;
-          ow[0] = pack2(d >= 0 ? w0 : 0.f, d >= 1 ? w1 : 0.f);
-          ow[1] = pack2(d >= 2 ? w2 : 0.f, d >= 3 ? w3 : 0.f);
+          ow[0] = pack2(d > 0 ? w0 : 0.f, d > 1 ? w1 : 0.f);
+          ow[1] = pack2(d > 2 ? w2 : 0.f, d > 3 ? w3 : 0.f);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, quad * 4 + i)) = o[i];
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (leader) tc::mma_commit(&gbar[wg]);
       if (it + 2 < m.i1) fetch_state(it + 2);
       if (!done.wait()) break;
-      const float Dh = D ? D[h] : 0.f;
+      const float Dh = fmaf(own[t], L.eta[t], D ? D[h] : 0.f);
       {
         float yi[32], yd[32];
         tc::tmem_ld32(lanes + kYi + half * 32, yi);
@@ -710,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[3 * kQ];
   __shared__ __align__(16) float tail[kQ];
-  __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[2][kQ],
+  __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[3][kQ],
       warp_ip[kThreads / 32];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
@@ -798,10 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     publish();
     if (threadIdx.x == 0) {
       const uint8_t* x2 = NB == 1 ? St + 4 * kTerm : Xs + kTerm;
-      for (int m = 0; m < 3; ++m) mma<kQ, false, kPT, true, NB * 64>(tmem, gs, St + m * kTerm, kPT / 16, m > 0);
-      mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, Xs, kPT / 16, false);
+      // the small terms first: the accumulator's cut-off bits then are the first term's alone
+      for (int m = 2; m >= 0; --m) mma<kQ, false, kPT, true, NB * 64>(tmem, gs, St + m * kTerm, kPT / 16, m < 2);
+      mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, x2, kPT / 16, false);
       mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, St + 3 * kTerm, kPT / 16, true);
-      mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, x2, kPT / 16, true);
+      mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, Xs, kPT / 16, true);
       tc::mma_commit(&bar);
     }
     fill_tails(L, tail);
@@ -852,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!(ok = done.wait())) break;
     if (it + 1 < i1) fetch_rows(it + 1, (it - i0 + 1) & 1);  // v has done its part
     // the decayed scores, and the row and column sums of Z off its diagonal
-    float zrow = 0.f, dr = 0.f, dd = 0.f;
+    float zrow = 0.f, dr = 0.f, dd = 0.f, dm = 0.f;
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       const int u0 = part * 32 + sub * 16;
@@ -899,12 +909,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           m[i] *= e[i];
           off[i] = m[i] * kk[i];
         }
+        if (part == quad && it == i0)  // q_t.k_t, the same for every item
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dm = u0 + i == t ? m[i] : dm;
         if (part == quad)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const bool on = u0 + i == t;
             dr = on ? off[i] : dr;
             dd = on ? kk[i] : dd;
+            m[i] = on ? 0.f : m[i];  // joins D in fp32
             off[i] = on ? 0.f : off[i];
           }
 #pragma unroll
@@ -930,6 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (part == quad) {  // the quarter that holds this row's diagonal block
       diag[0][t] = dr;
       diag[1][t] = dd;
+      if (it == i0) diag[2][t] = dm;
     }
     publish();
     if (threadIdx.x == 0) {
@@ -975,7 +990,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       after = lane < 31 ? after : 0.f;
       before = lane > 0 ? before : 0.f;
       const float through = L.from_start(kQ - 1) * ip, Ah = A[h];
-      float dl[4], dA = 0.f;
+      const double dA = decay_gradient<4>(a4, b4, L.eta + lane * 4, through, lane);
+      float dl[4];
 #pragma unroll
       for (int i = 3; i >= 0; --i) dl[i] = after += a4[i];
 #pragma unroll
@@ -987,18 +1003,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = lane * 4 + i;
-        dA = fmaf(L.eta[r], dl[i], dA);
         const float x = fmaf(Ah, dl[i], off4[i] + diag[0][r] + src4[i]);
         if (t0 + r < s.T) out[r] = r < n ? x : 0.f;
       }
 #pragma unroll
-      for (int d = 16; d; d >>= 1) {
-        dA += __shfl_xor_sync(~0u, dA, d);
-        dsum += __shfl_xor_sync(~0u, dsum, d);
-      }
+      for (int d = 16; d; d >>= 1) dsum += __shfl_xor_sync(~0u, dsum, d);
       if (lane == 0) {
         const long long at = ((long long)c * s.NPT + pt) * BH + bh;
-        o.dA[at] = dA;
+        o.dA[at] = (float)dA;
         o.dD[at] = dsum;
       }
       __syncwarp();
@@ -1008,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ld[2][16];
       tmem_ld16<2>({lanes + part * 16, lanes + 64 + part * 16}, ld);
       float(&a1)[16] = ld[0], (&a2)[16] = ld[1];
-      const float e = L.to_end(t), eta = L.eta[t], Dh = D ? D[h] : 0.f;
+      const float e = L.to_end(t), eta = L.eta[t], Dh = fmaf(eta, diag[2][t], D ? D[h] : 0.f);
       bf16* out = o.dv + vo + (long long)t * s.P + part * 16;
       if (t0 + t < s.T)
 #pragma unroll

@@ -152,7 +152,9 @@ __device__ __forceinline__ void load8f(float (&f)[8], const float* p, int left) 
   }
 }
 
-// f as three bf16 terms: f = t0 + t1 + t2 to 24 bits.
+// f as three bf16 terms, its mantissa's first, second and third eight bits: each is
+// what the ones before leave, cut off, so that the three add up to f exactly (above
+// the smallest exponents) and a term is the upper half of a word as it stands.
 __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
   uint32_t* o[3] = {&t[0].x, &t[1].x, &t[2].x};
 #pragma unroll
@@ -160,10 +162,10 @@ __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
     float a = f[2 * i], b = f[2 * i + 1];
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      const uint32_t p = pack2(a, b);
-      o[j][i] = p;
-      a -= lo_f(p);
-      b -= hi_f(p);
+      const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+      o[j][i] = __byte_perm(ua, ub, 0x7632);
+      a -= __uint_as_float(ua & 0xffff0000u);
+      b -= __uint_as_float(ub & 0xffff0000u);
     }
   }
 }
@@ -319,8 +321,8 @@ struct GroupMmas {
   uint32_t phase;
   int* status;
   int wg;
-  __device__ __forceinline__ bool wait() {
-    const bool ok = tc::mbar_wait(bar, phase);
+  __device__ __forceinline__ bool wait(bool so_far = true) {
+    const bool ok = tc::mbar_wait(bar, phase) && so_far;
     if (!ok) atomicExch(status, tc2::kErrMma);
     const bool all = group_and(wg, ok);
     if (!all) (void)tc::mbar_wait(bar, phase);
@@ -352,7 +354,9 @@ __device__ __forceinline__ void group_load_rows(uint8_t* tile, const bf16* src, 
 }
 
 struct Items {
-  int b, g, c, t0, n, i0, i1, HG;
+  int b, g, c, t0, n, i0, i1, HG, NPT;
+  __device__ __forceinline__ int head(int it) const { return g * HG + (NPT == 1 ? it : it / NPT); }
+  __device__ __forceinline__ int first_row(int it) const { return NPT == 1 ? 0 : it % NPT * kPT; }
 };
 __device__ __forceinline__ Items block_items(const SsmDims& s, const int* lengths, int per) {
   Items m;
@@ -360,6 +364,7 @@ __device__ __forceinline__ Items block_items(const SsmDims& s, const int* length
   m.b = blockIdx.y / s.G;
   m.g = blockIdx.y - m.b * s.G;
   m.HG = s.H / s.G;
+  m.NPT = s.NPT;
   m.t0 = m.c * kQ;
   m.n = min(max(ssm_row_length(lengths, m.b, s.T) - m.t0, 0), kQ);
   m.i0 = blockIdx.z * per;
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float hi = 0.f, lo = 0.f, eta = 0.f, end_hi = 0.f, end_lo = 0.f;
   // This thread's row of the item, and its token's logs.
   auto fetch = [&](int it) {
-    const int h = m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT, bh = m.b * s.H + h;
+    const int h = m.head(it), p0 = m.first_row(it), bh = m.b * s.H + h;
     const int np = min(kPT, s.P - p0);
     const bf16* xr = x + ((long long)bh * s.T + m.t0 + t) * s.P + p0;
     const float* lg = logs + ((long long)bh * s.NC + m.c) * 3 * kQ;
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (it + 2 < m.i1) fetch(it + 2);
     if (!done.wait()) break;
-    const int h = m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT, bh = m.b * s.H + h;
+    const int h = m.head(it), p0 = m.first_row(it), bh = m.b * s.H + h;
     const int np = min(kPT, s.P - p0);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     float* out = states + (((long long)m.c * s.B * s.H + bh) * s.P + p0 + half * 32) * s.N + t;
@@ -477,16 +482,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 // that are both at most one for a decaying state), so that only a quarter of the
 // decays takes an exponential each. A token's own term, W_tt v_t, joins D v_t in
 // fp32 instead: where it is most of y_t, y_t then has no rounding but its last.
+struct OutMaps {
+  CUtensorMap v, y, S;  // [B*H][T][P] (boxes of 128 x 64), and [NC*B*H][P][N] (64 x 64)
+};
 template <int NB, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     out_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,
                const bf16* __restrict__ v, const float* __restrict__ logs,
                const float* __restrict__ D, const int* __restrict__ lengths,
                const bf16* __restrict__ states, bf16* __restrict__ y, int per,
-               int* __restrict__ status) {
+               int* __restrict__ status, const __grid_constant__ OutMaps maps) {
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[2][3 * kQ], stail[2][kQ], own[kQ];
-  __shared__ uint64_t bar, gbar[2];
+  __shared__ uint64_t bar, gbar[2], sbar[2], full[2];
   __shared__ uint32_t slot;
   const int wg = threadIdx.x / kHalf, t = threadIdx.x % kQ, half = threadIdx.x / kQ & 1, quad = t >> 5;
   const bool leader = threadIdx.x % kHalf == 0;
@@ -495,10 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* Ws = ks + wg * kQ * 256;         // [kQ][kQ]
   uint8_t* Ss = ks + 2 * kQ * 256 + wg * NB * kPT * 128;                        // [64][NB * 64]
   uint8_t* vs = ks + 2 * kQ * 256 + 2 * NB * kPT * 128 + wg * 2 * kQ * 128;     // two of [kQ][64]
-  if (threadIdx.x == 0) {
-    tc::mbar_init(&gbar[0], 1);
-    tc::mbar_init(&gbar[1], 1);
-  }
+  if (threadIdx.x == 0)
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&gbar[i], 1);
+      tc::mbar_init(&sbar[i], 1);
+      tc::mbar_init(&full[i], 1);
+    }
   const uint32_t tmem = block_begin<512>(&bar, &slot);
   griddep_wait();
   griddep_launch_dependents();
@@ -508,26 +518,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   load_rows<kQ, NB, VEC>(ks, k + qo, s.N, m.n, s.N);
   float hi = 0.f, lo = 0.f, eta = 0.f;
   auto fetch_logs = [&](int it) {
-    const float* lg = logs + ((long long)(m.b * s.H + m.g * m.HG + it / s.NPT) * s.NC + m.c) * 3 * kQ;
+    const float* lg = logs + ((long long)(m.b * s.H + m.head(it)) * s.NC + m.c) * 3 * kQ;
     hi = lg[t];
     lo = lg[kQ + t];
     eta = lg[2 * kQ + t];
   };
+  // An item's state and rows: by TMA where a row of the tile is either a token that
+  // exists or beyond T (which reads as zero), else by the group's threads.
+  const bool tma = VEC && m.n == min(kQ, s.T - m.t0);
   auto fetch_state = [&](int it) {
-    const int bh = m.b * s.H + m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT;
-    group_load_rows<kPT, NB, VEC>(Ss, states + (((long long)m.c * s.B * s.H + bh) * s.P + p0) * s.N, s.N,
-                                  min(kPT, s.P - p0), s.N);
+    const int bh = m.b * s.H + m.head(it), p0 = m.first_row(it);
+    if (tma) {
+      if (leader)
+        for (int i = 0; i < NB; ++i)
+          tc::tma_load_3d(Ss + i * kPT * 128, &maps.S, &full[wg], i * 64, p0, m.c * s.B * s.H + bh);
+    } else {
+      group_load_rows<kPT, NB, VEC>(Ss, states + (((long long)m.c * s.B * s.H + bh) * s.P + p0) * s.N, s.N,
+                                    min(kPT, s.P - p0), s.N);
+    }
   };
   auto fetch_rows = [&](int it, int buf) {
-    const int bh = m.b * s.H + m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT;
-    group_load_rows<kQ, 1, VEC>(vs + buf * kQ * 128, v + ((long long)bh * s.T + m.t0) * s.P + p0, s.P, m.n,
-                                min(kPT, s.P - p0));
+    const int bh = m.b * s.H + m.head(it), p0 = m.first_row(it);
+    if (tma) {
+      if (leader) {
+        tc::mbar_expect_tx(&full[wg], kQ * 128 + NB * kPT * 128);  // of the state too
+        tc::tma_load_3d(vs + buf * kQ * 128, &maps.v, &full[wg], p0, m.t0, bh);
+      }
+    } else {
+      group_load_rows<kQ, 1, VEC>(vs + buf * kQ * 128, v + ((long long)bh * s.T + m.t0) * s.P + p0, s.P, m.n,
+                                  min(kPT, s.P - p0));
+    }
   };
   int it = m.i0 + wg;
   if (it < m.i1) {
     fetch_logs(it);
-    fetch_state(it);
     fetch_rows(it, 0);
+    fetch_state(it);
   }
   cp_wait();
   publish();
@@ -557,9 +583,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const ChunkLogs L = logs_view(slog[wg]);
     float* tail = stail[wg];
     int buf = 0;
+    uint32_t phase = 0;  // of the loads and of the state's product
+    bool lead_ok = true, gave_up = false;
 #pragma unroll 1
     for (; it < m.i1; it += 2, buf ^= 1) {
-      const int h = m.g * m.HG + it / s.NPT, p0 = it % s.NPT * kPT, bh = m.b * s.H + h;
+      const int h = m.head(it), p0 = m.first_row(it), bh = m.b * s.H + h;
       const int np = min(kPT, s.P - p0);
       const float tl = ex2((__shfl_sync(~0u, hi, 31) - hi) + (__shfl_sync(~0u, lo, 31) - lo)) * eta;
       if (half == 0) {
@@ -570,13 +598,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float f = ex2(hi + lo), thi = hi, tlo = lo;
       cp_wait();
-      group_publish(wg);  // the item's rows, state and logs are there
+      group_publish(wg);  // the item's logs, and what the threads loaded, are there
       if (leader) {
+        lead_ok = !tma || tc::mbar_wait(&full[wg], phase);
         mma<kQ, false, kPT, false, 64>(tmem + kYi, qs, Ss, nsteps, false);
-        tc::mma_commit(&gbar[wg]);
+        tc::mma_commit(&sbar[wg]);
       }
       if (it + 2 < m.i1) {
         fetch_logs(it + 2);
+        if (tma && leader) tc::bulk_wait_read<0>();  // that buffer's y is on its way
         fetch_rows(it + 2, buf ^ 1);
       }
 #pragma unroll 1
@@ -619,11 +649,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       group_publish(wg);
       uint8_t* vb = vs + buf * kQ * 128;
-      if (leader) mma<kQ, false, kQ, true, 64>(tmem + kYd, Ws, vb, kQ / 16, false);
-      if (!done.wait()) break;  // of the state's product: its tile is free
-      if (leader) tc::mma_commit(&gbar[wg]);
+      if (leader) {
+        mma<kQ, false, kQ, true, 64>(tmem + kYd, Ws, vb, kQ / 16, false);
+        tc::mma_commit(&gbar[wg]);
+      }
+      if (!tma || leader) lead_ok = tc::mbar_wait(&sbar[wg], phase) && lead_ok;  // the state's tile is free
       if (it + 2 < m.i1) fetch_state(it + 2);
-      if (!done.wait()) break;
+      if (!done.wait(lead_ok)) {
+        gave_up = true;
+        break;
+      }
+      // (v has landed: the leader saw it before the group last met)
+      phase ^= 1u;
       const float Dh = fmaf(own[t], L.eta[t], D ? D[h] : 0.f);
       {
         float yi[32], yd[32];
@@ -647,22 +684,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           *at = o;  // y takes the place of v
         }
       }
-      tc::tc_fence_before();
-      group_sync(wg);
-      tc::tc_fence_after();
-      // whole rows to memory: eight threads a row
-      bf16* out = y + ((long long)bh * s.T + m.t0) * s.P + p0;
-      const int j = t & 7, r0 = threadIdx.x % kHalf >> 3, rows = s.T - m.t0;
-      uint4 o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const uint4*>(vb + piece<kQ>(r0, j) + i * 32 * 128);
-      out += (long long)r0 * s.P + j * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (r0 + i * 32 < rows) store8<VEC>(out, o[i], np - j * 8);
-        out += 32 * (long long)s.P;
+      if constexpr (VEC) {
+        group_publish(wg);
+        if (leader) {  // rows beyond T and columns beyond P are not written
+          tc::tma_store_3d(&maps.y, vb, p0, m.t0, bh);
+          tc::bulk_commit();
+          if (!tma) tc::bulk_wait_read<0>();
+        }
+        if (!tma) group_sync(wg);
+      } else {
+        tc::tc_fence_before();
+        group_sync(wg);
+        tc::tc_fence_after();
+        // whole rows to memory: eight threads a row
+        const int j = t & 7, r0 = threadIdx.x % kHalf >> 3;
+        bf16* out = y + ((long long)bh * s.T + m.t0 + r0) * s.P + p0 + j * 8;
+        for (int i = 0; i < 4; ++i)
+          if (m.t0 + r0 + i * 32 < s.T)
+            store8<VEC>(out + i * 32 * (long long)s.P,
+                        *reinterpret_cast<const uint4*>(vb + piece<kQ>(r0, j) + i * 32 * 128), np - j * 8);
       }
     }
+    if (leader) {
+      tc::bulk_wait_all();
+      if (tma && gave_up)  // no load of ours may outlive the block
+        for (uint32_t i = 0; i < 2; ++i) (void)tc::mbar_wait(&full[wg], phase ^ i);
+    }
+  } else if (tma && leader && it < m.i1) {
+    (void)tc::mbar_wait(&full[wg], 0u);
   }
   block_end<512>(tmem);
 }
@@ -1124,6 +1173,32 @@ dim3 item_grid(const SsmDims& s, int parts, int* per) {
   return dim3(s.NC, s.B * s.G, parts);
 }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(ptr);
+  }();
+  return fn;
+}
+// Matrices [count][rows][cols] of bf16 in boxes of box_rows x 64, 128-byte swizzle;
+// what lies outside a matrix reads as zero and is not written.
+bool tile_map(CUtensorMap* m, const void* base, uint64_t count, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cols, rows, count}, strides[2] = {cols * 2, rows * cols * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class F>
 cudaError_t allow_smem(F* f, size_t bytes) {
   return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
@@ -1209,9 +1284,13 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
                         : (vec ? out_kernel<2, true> : out_kernel<2, false>);
   const size_t smem = s.N <= 64 ? out_smem<1>() : out_smem<2>();
   if ((e = allow_smem(kern, smem)) != cudaSuccess) return e;
+  OutMaps maps = {};
+  if (vec && !(tile_map(&maps.v, a.v, BH, s.T, s.P, kQ) && tile_map(&maps.y, a.y, BH, s.T, s.P, kQ) &&
+               tile_map(&maps.S, a.starts, (uint64_t)s.NC * BH, s.P, s.N, kPT)))
+    return cudaErrorNotSupported;
   return launch_pdl(kern, grid, dim3(kThreads), smem, a.st, s, (const bf16*)a.q, (const bf16*)a.k,
                     (const bf16*)a.v, (const float*)a.logs, a.D, a.lengths, (const bf16*)a.starts,
-                    (bf16*)a.y, per, a.status);
+                    (bf16*)a.y, per, a.status, maps);
 }
 
 }  // namespace e2ttt

@@ -376,28 +376,29 @@ __device__ __forceinline__ Items block_items(const SsmDims& s, const int* length
 // states[c][bh][p][n] = sum_s w_s x_s[p] y_s[n]: with REV 0 x = v, y = k,
 // w_s = e^{c_Q-c_s} eta_s; with REV 1 x = dy, y = q, w_t = e^{c_t}. D[n][p] on
 // the tensor cores: y contracted over its rows (128 state columns as rows of the
-// tile), against the three terms of w x side by side, so that y is read once for
-// all three (N = 192: 80 cycles of shared-memory reads a step instead of 144).
+// tile), against the three terms of w x one after another. An item is a chain of
+// short steps (loads, the split, the MMAs, the stores), so three streams of items
+// share the block.
+constexpr int kStateStreams = 3;
 template <int REV, bool VEC>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kStateStreams * kHalf, 1)
     state_kernel(SsmDims s, const bf16* __restrict__ x, const bf16* __restrict__ y,
                  const float* __restrict__ logs, const int* __restrict__ lengths,
                  float* __restrict__ states, int per, int* __restrict__ status) {
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bar, gbar[2];
+  __shared__ uint64_t bar, gbar[kStateStreams];
   __shared__ uint32_t slot;
   uint8_t* ys = align1k(raw);  // [kQ][128]
   const int wg = threadIdx.x / kHalf, t = threadIdx.x % kQ, half = threadIdx.x / kQ & 1, quad = t >> 5;
   uint8_t* xs = ys + kQ * 256 + wg * 3 * kQ * 128;  // three of [kQ][64]
-  if (threadIdx.x == 0) {
-    tc::mbar_init(&gbar[0], 1);
-    tc::mbar_init(&gbar[1], 1);
-  }
-  const uint32_t tmem = block_begin<512>(&bar, &slot) + wg * 192;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kStateStreams; ++i) tc::mbar_init(&gbar[i], 1);
+  const uint32_t tmem = block_begin<256>(&bar, &slot) + wg * 64;
   griddep_wait();
   griddep_launch_dependents();
   const Items m = block_items(s, lengths, per);
-  load_rows<kQ, 2, VEC>(ys, y + (((long long)m.b * s.G + m.g) * s.T + m.t0) * s.N, s.N, m.n, s.N);
+  if (threadIdx.x < kThreads)
+    load_rows<kQ, 2, VEC>(ys, y + (((long long)m.b * s.G + m.g) * s.T + m.t0) * s.N, s.N, m.n, s.N);
   uint4 xv[4];
   float hi = 0.f, lo = 0.f, eta = 0.f, end_hi = 0.f, end_lo = 0.f;
   // This thread's row of the item, and its token's logs.
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   publish();
   GroupMmas done{&gbar[wg], 0u, status, wg};
 #pragma unroll 1
-  for (; it < m.i1; it += 2) {
+  for (; it < m.i1; it += kStateStreams) {
     const float w = REV ? ex2(hi + lo) : ex2((end_hi - hi) + (end_lo - lo)) * eta;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -444,24 +445,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     group_publish(wg);
     if (threadIdx.x % kHalf == 0) {
-      mma<kQ, true, kQ, true, 192>(tmem, ys, xs, kQ / 16, false);
+      for (int i = 2; i >= 0; --i) mma<kQ, true, kQ, true, 64>(tmem, ys, xs + i * kQ * 128, kQ / 16, i < 2);
       tc::mma_commit(&gbar[wg]);
     }
-    if (it + 2 < m.i1) fetch(it + 2);
+    if (it + kStateStreams < m.i1) fetch(it + kStateStreams);
     if (!done.wait()) break;
     const int h = m.head(it), p0 = m.first_row(it), bh = m.b * s.H + h;
     const int np = min(kPT, s.P - p0);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     float* out = states + (((long long)m.c * s.B * s.H + bh) * s.P + p0 + half * 32) * s.N + t;
     if (quad * 32 < s.N) {
-#pragma unroll 1
+#pragma unroll
       for (int cb = half * 32; cb < half * 32 + 32; cb += 16) {
-        float ld[3][16];
-        tmem_ld16<3>({lanes + cb, lanes + 64 + cb, lanes + 128 + cb}, ld);
+        float ld[1][16];
+        tmem_ld16<1>({lanes + cb}, ld);
         const int left = t < s.N ? np - cb : 0;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          if (j < left) *out = ld[0][j] + (ld[1][j] + ld[2][j]);
+          if (j < left) *out = ld[0][j];
           out += s.N;
         }
       }
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     group_sync(wg);  // the accumulators are read before the next item's MMAs write them
     tc::tc_fence_after();
   }
-  block_end<512>(tmem - wg * 192);
+  block_end<256>(tmem - wg * 64);
 }
 
 // ------------------------------------------------------------------ outputs
@@ -1135,7 +1136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   block_end<512>(tmem);
 }
 
-size_t state_smem() { return 1024 + kQ * 256 + 2 * 3 * kQ * 128; }
+size_t state_smem() { return 1024 + kQ * 256 + kStateStreams * 3 * kQ * 128; }
 template <int NB>
 size_t out_smem() {
   return 1024 + NB * kQ * 128 + 2 * kQ * 256 + 2 * NB * kPT * 128 + 4 * kQ * 128;
@@ -1235,8 +1236,8 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
     E2TTT_TRACE("ssm_chunk_dstate", a.st);
     auto kern = vec ? state_kernel<1, true> : state_kernel<1, false>;
     if ((e = allow_smem(kern, state_smem())) != cudaSuccess) return e;
-    const dim3 grid = item_grid(s, item_parts(s, 2, 1.5, 0), &per);
-    e = launch_pdl(kern, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.dy, (const bf16*)a.q,
+    const dim3 grid = item_grid(s, item_parts(s, kStateStreams, 1.5, 0), &per);
+    e = launch_pdl(kern, grid, dim3(kStateStreams * kHalf), state_smem(), a.st, s, (const bf16*)a.dy, (const bf16*)a.q,
                    (const float*)w.logs, a.lengths, w.ends, per, w.status);
     if (e != cudaSuccess) return e;
   }
@@ -1261,7 +1262,6 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
   const SsmDims& s = a.s;
   const int BH = s.B * s.H;
   int per = 0;
-  const dim3 grid = item_grid(s, item_parts(s, 2, 1.5, 0), &per);
   const bool vec = vectors(s, {a.q, a.k, a.v, a.y});
   cudaError_t e;
   {
@@ -1274,7 +1274,8 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
     E2TTT_TRACE("ssm_chunk_state", a.st);
     auto kern = vec ? state_kernel<0, true> : state_kernel<0, false>;
     if ((e = allow_smem(kern, state_smem())) != cudaSuccess) return e;
-    e = launch_pdl(kern, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.v, (const bf16*)a.k,
+    const dim3 grid = item_grid(s, item_parts(s, kStateStreams, 1.5, 0), &per);
+    e = launch_pdl(kern, grid, dim3(kStateStreams * kHalf), state_smem(), a.st, s, (const bf16*)a.v, (const bf16*)a.k,
                    (const float*)a.logs, a.lengths, a.states, per, a.status);
     if (e != cudaSuccess) return e;
   }
@@ -1284,6 +1285,7 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
                         : (vec ? out_kernel<2, true> : out_kernel<2, false>);
   const size_t smem = s.N <= 64 ? out_smem<1>() : out_smem<2>();
   if ((e = allow_smem(kern, smem)) != cudaSuccess) return e;
+  const dim3 grid = item_grid(s, item_parts(s, 2, 1.5, 0), &per);
   OutMaps maps = {};
   if (vec && !(tile_map(&maps.v, a.v, BH, s.T, s.P, kQ) && tile_map(&maps.y, a.y, BH, s.T, s.P, kQ) &&
                tile_map(&maps.S, a.starts, (uint64_t)s.NC * BH, s.P, s.N, kPT)))

@@ -4,7 +4,7 @@
 //
 // Bound by HBM: the norm reads every gradient once; the clip reads them again
 // and writes them, and reads nothing where the norm is within max_norm and the
-// clip is in place. The tensors are cut into pieces of kPiece elements; block i
+// clip is in place. The tensors are cut into pieces of kPieceBytes; block i
 // takes an equal range of the pieces of the whole list, so one launch serves
 // many small tensors as well as a few large ones (the list travels as a kernel
 // parameter, kMany tensors to a launch). Squares are summed in fp32 over one
@@ -20,7 +20,9 @@ namespace e2ttt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 16384;
+// Pieces of equal bytes, so that the blocks' shares are alike whatever the types.
+constexpr int kPieceBytes = 32768;
+template <typename T> constexpr int kPiece = kPieceBytes / sizeof(T);
 constexpr int kFew = 32, kMany = 480;
 
 struct Item {
@@ -75,8 +77,8 @@ __device__ __forceinline__ double square1(T v) {
 template <typename T>
 __device__ double piece_squares(const Item& it, unsigned piece) {
   constexpr int N = Wide<T>::N;
-  const unsigned long long beg = (unsigned long long)piece * kPiece;
-  const int n = (int)(it.n - beg < kPiece ? it.n - beg : kPiece);
+  const unsigned long long beg = (unsigned long long)piece * kPiece<T>;
+  const int n = (int)(it.n - beg < kPiece<T> ? it.n - beg : kPiece<T>);
   const T* g = (const T*)it.g + beg;
   double a = 0.0;
   // elements before the first 16-byte boundary, whole vectors, the rest
@@ -152,8 +154,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* __res
 template <typename T>
 __device__ void piece_scale(const Item& it, unsigned piece, float scale) {
   constexpr int N = Wide<T>::N;
-  const unsigned long long beg = (unsigned long long)piece * kPiece;
-  const int n = (int)(it.n - beg < kPiece ? it.n - beg : kPiece);
+  const unsigned long long beg = (unsigned long long)piece * kPiece<T>;
+  const int n = (int)(it.n - beg < kPiece<T> ? it.n - beg : kPiece<T>);
   const T* g = (const T*)it.g + beg;
   T* o = (T*)it.out + beg;
   const bool same = (((uintptr_t)g ^ (uintptr_t)o) & 15) == 0;
@@ -209,7 +211,8 @@ int take(const GradList& g, int at, List<MAX>* l) {
   l->pieces = 0;
   for (; at < g.count && l->count < MAX; ++at) {
     if (!g.n[at]) continue;
-    const unsigned long long pieces = (g.n[at] + kPiece - 1) / kPiece;
+    const int each = g.act[at] == 1 ? kPiece<bf16> : kPiece<float>;
+    const unsigned long long pieces = (g.n[at] + each - 1) / each;
     if (l->count && pieces + l->pieces > 0x7fffffffull) break;
     l->t[l->count++] = Item{g.g[at], g.out && g.out[at] ? g.out[at] : const_cast<void*>(g.g[at]),
                             (unsigned long long)g.n[at], l->pieces, (unsigned)(g.act[at] == 1)};

@@ -290,7 +290,8 @@ e2ttt_status e2ttt_chunk_scan_bwd(const e2ttt_shape* shape,
  *   x [B, H, T, d] (act dtype), w [H, d, W] fp32, bias [H, d] fp32 or NULL
  *   state [B, H, W-1, d] (act dtype) or NULL: the W-1 inputs before the first
  *   token, oldest first; NULL stands for zeros.
- * Limits: all sizes >= 1, W <= 8, B*H <= 65535, T <= 2^24, H*d*W < 2^31. */
+ * Limits: all sizes >= 1, W <= 8, d <= 2^20, B*H <= 65535, T <= 2^24,
+ * H*d*W < 2^31. */
 typedef struct {
   int B, H, T, d, W;
   int act;  /* e2ttt_dtype */
@@ -336,7 +337,7 @@ e2ttt_status e2ttt_short_conv_step(const e2ttt_conv_shape* shape, const void* x,
  * cores. The waits of the tensor-core kernels are bounded:
  * e2ttt_workspace_status(workspace) reports one that gave up.
  * Limits: all sizes >= 1, H a multiple of G, d_k <= 256, d_v <= 1024,
- * B*H <= 65535, T <= 2^24. */
+ * B*H <= 65535, T <= 2^24, ceil(T/32)*B*H*ceil(d_v/64) < 2^31. */
 typedef struct {
   int B, H, G, T;
   int d_k, d_v;

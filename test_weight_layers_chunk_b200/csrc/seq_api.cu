@@ -56,8 +56,8 @@ e2ttt_status conv_dims(const char* who, const e2ttt_conv_shape* s, ConvDims* d) 
   if ((long long)s->B * s->H > 65535)
     return failf(E2TTT_ERR_INVALID_ARG, "%s: B*H must be <= 65535", who);
   if (s->T > (1 << 24)) return failf(E2TTT_ERR_INVALID_ARG, "%s: T must be <= 2^24", who);
-  if ((long long)s->H * s->d * s->W >= (1LL << 31))
-    return failf(E2TTT_ERR_INVALID_ARG, "%s: H*d*W must be < 2^31", who);
+  if (s->d > (1 << 20) || (long long)s->H * s->d * s->W >= (1LL << 31))
+    return failf(E2TTT_ERR_INVALID_ARG, "%s: d must be <= 2^20 and H*d*W < 2^31", who);
   *d = ConvDims{s->B, s->H, s->T, s->d, s->W, s->act == E2TTT_BF16, s->silu == 1};
   return E2TTT_OK;
 }
@@ -103,6 +103,8 @@ e2ttt_status ssm_dims(const char* who, const e2ttt_ssm_shape* s, SsmDims* d) {
   d->Q = d->tc ? kSsmTcChunk : s->d_k <= 128 ? 64 : 32;
   d->NC = (s->T + d->Q - 1) / d->Q;
   d->NPT = (s->d_v + kSsmPT - 1) / kSsmPT;
+  if ((long long)d->NC * s->B * s->H * d->NPT >= (1LL << 31))
+    return failf(E2TTT_ERR_INVALID_ARG, "%s: too many chunks: ceil(T/%d)*B*H*ceil(d_v/64) must be < 2^31", who, d->Q);
   return E2TTT_OK;
 }
 

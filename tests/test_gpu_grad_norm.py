@@ -76,6 +76,11 @@ def test_within_the_norm_nothing_changes(E):
     assert all(torch.equal(a, b) for a, b in zip(grads, keep))
 
 
+def test_empty_tensors_only(E):
+    grads = [torch.empty(0, device="cuda"), torch.empty(0, device="cuda", dtype=torch.bfloat16)]
+    assert float(E.clip_grad_norm(grads, 1.0)) == 0.0 and float(E.grad_norm(grads)) == 0.0
+
+
 def test_large_and_small_values(E):
     """Squares beyond fp32's range, and below it."""
     for scale in (1e30, 1e-30, 1e-42):

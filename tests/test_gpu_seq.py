@@ -400,6 +400,33 @@ def test_scan_graph_and_streams(E):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("act,N", [("bf16", 64), ("f32", 64), ("bf16", 200)])
+def test_scan_workspace_and_status(E, act, N):
+    """A caller's workspace, whatever it holds; its status word says that no wait gave up."""
+    x = scan_inputs(act, 1, 2, 1, 150, 64, N, True, True, True, seed=16)
+    g, _ = to_gpu(x, None, 150)
+    want = run_scan(E, g, None)
+    shape = E.make_ssm_shape(1, 2, 1, 150, N, 64, E.BF16 if act == "bf16" else E.F32)
+    for fill in (0xff, 0x7f):
+        ws = [torch.full((E.e2ttt_ssm_workspace_bytes(shape, i),), fill, dtype=torch.uint8, device="cuda") for i in (0, 1)]
+        y, S, saved = E.ssm_scan_fwd(g["q"], g["k"], g["v"], g["dt"], g["A"], g["D"], g["S0"], save_states=True, ws=ws[0])
+        assert E.e2ttt_workspace_status(ws[0], raw=True, stream=torch.cuda.current_stream().cuda_stream) == E.OK
+        grads = E.ssm_scan_bwd(g["q"], g["k"], g["v"], g["dt"], g["A"], saved, g["dy"], g["D"], g["dS_end"], ws=ws[1])
+        assert E.e2ttt_workspace_status(ws[1], raw=True, stream=torch.cuda.current_stream().cuda_stream) == E.OK
+        assert torch.equal(y, want[0]) and torch.equal(S, want[1])
+        for n, t in grads.items():
+            assert torch.equal(t, want[2][n]), n
+
+
+def test_scan_many_state_tiles_and_long_rows(E):
+    """Sixteen tiles of state rows, and more chunks than one batch of the carry."""
+    for act, B, H, G, T, P, N in (("bf16", 1, 2, 1, 130, 1024, 16), ("f32", 1, 1, 1, 70, 520, 8), ("bf16", 1, 1, 1, 2300, 16, 16),
+                                  ("f32", 1, 1, 1, 1200, 8, 8)):
+        x = scan_inputs(act, B, H, G, T, P, N, True, True, True, seed=T)
+        g, _ = to_gpu(x, None, T)
+        scan_check(act, x, None, *run_scan(E, g, None))
+
+
 # ------------------------------------------------------------------ refusals that need a device
 def test_conveniences_refuse(E):
     x = scan_inputs("bf16", 1, 4, 2, 8, 16, 16, True, True, True, seed=1)

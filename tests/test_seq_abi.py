@@ -43,7 +43,7 @@ def _refused(E, st, *words):
 def test_conv_shapes(E):
     ok = dict(B=2, H=3, T=5, d=8, W=4)
     for over in (dict(B=0), dict(H=0), dict(T=0), dict(d=0), dict(W=0), dict(W=9), dict(act=2), dict(B=70000),
-                 dict(T=(1 << 24) + 1), dict(H=60000, B=1, d=1 << 15)):
+                 dict(T=(1 << 24) + 1), dict(H=60000, B=1, d=1 << 15), dict(d=(1 << 20) + 1)):
         s = E.make_conv_shape(**(ok | over))
         assert E.e2ttt_short_conv_workspace_bytes(s) == 0
         for fn in ("fwd", "bwd"):
@@ -79,7 +79,8 @@ def test_conv_arguments(E):
 def test_scan_shapes(E):
     ok = dict(B=2, H=4, G=2, T=70, d_k=16, d_v=8)
     for over in (dict(B=0), dict(H=0), dict(G=0), dict(G=3), dict(T=0), dict(d_k=0), dict(d_v=0), dict(d_k=257),
-                 dict(d_v=1025), dict(act=5), dict(B=40000), dict(T=(1 << 24) + 1)):
+                 dict(d_v=1025), dict(act=5), dict(B=40000), dict(T=(1 << 24) + 1),
+                 dict(B=16000, T=1 << 24)):
         s = E.make_ssm_shape(**(ok | over))
         assert E.e2ttt_ssm_workspace_bytes(s, 0) == E.e2ttt_ssm_workspace_bytes(s, 1) == 0
         assert E.e2ttt_ssm_saved_bytes(s) == 0

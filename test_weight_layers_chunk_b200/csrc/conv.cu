@@ -155,17 +155,53 @@ __device__ __forceinline__ void load_seq(const T* xrow, const T* srow, int i, in
     zero(f);
 }
 
-// N raw rows of a token matrix from p on.
-template <typename V, typename T, int N>
-__device__ __forceinline__ void load_batch(V (&raw)[N], const T* p, int d) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    raw[i] = *reinterpret_cast<const V*>(p);
-    p += d;
-  }
-}
+constexpr int kBatch = 4;   // tokens that are computed together
 
-constexpr int kBatch = 4;  // tokens whose loads are in flight together
+// A thread's own ring of raw rows in shared memory, filled by asynchronous copies
+// several batches ahead without holding registers; no other thread reads it, so it
+// needs no barrier. Single channels of two bytes are too small for such copies and
+// are loaded when they are needed.
+template <typename T, int VEC, int STREAMS>
+struct Ring {
+  typedef typename VecOf<T, VEC>::type V;
+  static constexpr bool kAsync = sizeof(V) >= 4;
+  // Batches whose loads are in flight beyond the current one (two of 16 bytes keep a
+  // block's ring within the 48 KB that need no asking for).
+  static constexpr int kAhead = sizeof(V) == 16 ? 2 : 3, kRing = kAhead + 1;
+  V* slots;  // [kRing][STREAMS][kBatch][threads]
+  int threads;
+  __device__ __forceinline__ V* slot(int batch, int stream, int i) const {
+    return slots + (((batch % kRing) * STREAMS + stream) * kBatch + i) * threads + threadIdx.x;
+  }
+  // Rows p, p + d, .. of one batch.
+  __device__ __forceinline__ void copy(int batch, int stream, const T* p, int d) const {
+    if constexpr (kAsync) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot(batch, stream, i));
+        if constexpr (sizeof(V) == 16)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(p), "n"(sizeof(V)) : "memory");
+        p += d;
+      }
+    }
+  }
+  // Ends one batch of copies (an empty one too: the groups are counted).
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // The batch that was committed kAhead batches before the last one has landed.
+  __device__ __forceinline__ void landed() const { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory"); }
+  __device__ __forceinline__ void read(V (&raw)[kBatch], int batch, int stream, const T* p, int d) const {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if constexpr (kAsync)
+        raw[i] = *slot(batch, stream, i);
+      else
+        raw[i] = *reinterpret_cast<const V*>(p);
+      p += d;
+    }
+  }
+};
 
 template <typename T, int W, int VEC, bool SILU>
 __global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 2) conv_fwd_kernel(Geo g, const T* __restrict__ x,
@@ -190,8 +226,16 @@ __global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 2) conv_fwd_kernel(Geo 
 
   const T* xp = xrow + (long long)t0 * g.d + c0;
   T* yp = yrow + (long long)t0 * g.d + c0;
-  V next[kBatch];
-  if (full) load_batch(next, xp, g.d);
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
+  typedef Ring<T, VEC, 1> R;
+  constexpr int kAhead = R::kAhead;
+  const R ring{reinterpret_cast<V*>(ring_bytes), (int)blockDim.x};
+  const long long step = (long long)kBatch * g.d;
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) {
+    if (n < full) ring.copy(n, 0, xp + n * step, g.d);
+    ring.commit();
+  }
   F2 wr[W][NP], br[NP];
   load_taps<W, VEC>(w + ((long long)h * g.d + c0) * W, wr);
   load_bias<VEC>(bias ? bias + h * g.d + c0 : nullptr, br);
@@ -213,11 +257,12 @@ __global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 2) conv_fwd_kernel(Geo 
   };
 #pragma unroll 1
   for (int n = 0; n < full; ++n) {
+    if (n + kAhead < full) ring.copy(n + kAhead, 0, xp + kAhead * step, g.d);
+    ring.commit();
+    ring.landed();
     V raw[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
-    xp += (long long)kBatch * g.d;
-    if (n + 1 < full) load_batch(next, xp, g.d);
+    ring.read(raw, n, 0, xp, g.d);
+    xp += step;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       F2 o[NP];
@@ -258,7 +303,12 @@ __global__ void __launch_bounds__(kThreads, W <= 4 ? 2 : 1)
                     float* __restrict__ part) {
   typedef typename VecOf<T, VEC>::type V;
   constexpr int W1 = W - 1, NP = (VEC + 1) / 2;
-  extern __shared__ float sums[];  // [blockDim.x][VEC]
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
+  float* sums = reinterpret_cast<float*>(ring_bytes);  // [blockDim.x][VEC], after the runs
+  typedef Ring<T, VEC, 2> R;
+  constexpr int kAhead = R::kAhead;
+  const R ring{reinterpret_cast<V*>(ring_bytes), (int)blockDim.x};
+  const long long step = (long long)kBatch * g.d;
   const int bh = blockIdx.y, h = bh % g.H, b = bh / g.H;
   const int vl = threadIdx.x % g.nvt, vi = blockIdx.z * g.nvt + vl, c0 = vi * VEC;
   const bool on = vi < g.nvec;
@@ -283,10 +333,13 @@ __global__ void __launch_bounds__(kThreads, W <= 4 ? 2 : 1)
     const int end = min(t1, len), full = end > t0 ? (end - t0) / kBatch : 0;
     const T* xp = xrow + (long long)t0 * g.d + c0;
     const T* gp = dyrow + (long long)t0 * g.d + c0;
-    V nx[kBatch], nd[kBatch];
-    if (full) {
-      load_batch(nx, xp, g.d);
-      load_batch(nd, gp, g.d);
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      if (n < full) {
+        ring.copy(n, 0, xp + n * step, g.d);
+        ring.copy(n, 1, gp + n * step, g.d);
+      }
+      ring.commit();
     }
     F2 win[W][NP], dz[W][NP];  // dz[j]: of the token j before the current one
 #pragma unroll
@@ -329,15 +382,17 @@ __global__ void __launch_bounds__(kThreads, W <= 4 ? 2 : 1)
     T* op = dxrow + (long long)(t0 - W1) * g.d + c0;  // where token s's o goes
 #pragma unroll 1
     for (int n = 0; n < full; ++n) {
-      V rx[kBatch], rd[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) rx[i] = nx[i], rd[i] = nd[i];
-      xp += (long long)kBatch * g.d;
-      gp += (long long)kBatch * g.d;
-      if (n + 1 < full) {
-        load_batch(nx, xp, g.d);
-        load_batch(nd, gp, g.d);
+      if (n + kAhead < full) {
+        ring.copy(n + kAhead, 0, xp + kAhead * step, g.d);
+        ring.copy(n + kAhead, 1, gp + kAhead * step, g.d);
       }
+      ring.commit();
+      ring.landed();
+      V rx[kBatch], rd[kBatch];
+      ring.read(rx, n, 0, xp, g.d);
+      ring.read(rd, n, 1, gp, g.d);
+      xp += step;
+      gp += step;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         F2 o[NP];
@@ -469,7 +524,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int j = 0; j < W1; ++j) *reinterpret_cast<V*>(srow + (long long)j * d) = raw[j + 1];
 }
 
-Geo geometry(const ConvDims& s, int vec) {
+Geo geometry(const ConvDims& s, int vec, bool back) {
   Geo g{};
   g.H = s.H;
   g.T = s.T;
@@ -477,10 +532,12 @@ Geo geometry(const ConvDims& s, int vec) {
   g.nvec = s.d / vec;
   g.nvt = g.nvec < kThreads ? g.nvec : kThreads;
   g.rows = kThreads / g.nvt;
-  // Long runs re-read and recompute less (W - 1 tokens a run); short ones give
-  // more threads. The longest that still gives every SM 768 threads.
-  g.R = 32;
-  while (g.R > 8 && (long long)s.B * s.H * g.nvec * ((s.T + g.R - 1) / g.R) < 148LL * 768) g.R /= 2;
+  // Long runs re-read and recompute less (W - 1 tokens a run, which the backward
+  // walks twice); short ones give more threads. The longest that still gives every
+  // SM 768 threads, in the backward (half as many fit) 384.
+  g.R = back ? 64 : 32;
+  const long long enough = 148LL * (back ? 384 : 768);
+  while (g.R > 8 && (long long)s.B * s.H * g.nvec * ((s.T + g.R - 1) / g.R) < enough) g.R /= 2;
   g.runs = (s.T + g.R - 1) / g.R;
   return g;
 }
@@ -494,13 +551,32 @@ int bwd_blocks_x(const ConvDims& s, const Geo& g) {
   return (int)(tiles < want ? tiles : want);
 }
 
+// Shared memory of a block: its ring, or the sums that follow it.
+template <typename T, int VEC, int STREAMS>
+size_t ring_bytes(int threads) {
+  typedef Ring<T, VEC, STREAMS> R;
+  const size_t ring = R::kAsync ? sizeof(typename R::V) * R::kRing * STREAMS * kBatch * threads : 0;
+  const size_t sums = sizeof(float) * VEC * threads;
+  return ring > sums ? ring : sums;
+}
+
+template <class F>
+cudaError_t allow_smem(F* f, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 template <typename T, int W, int VEC>
 cudaError_t fwd_t(const ConvArgs& a, void* y, void* state_end) {
-  const Geo g = geometry(a.s, VEC);
+  const Geo g = geometry(a.s, VEC, false);
   dim3 grid((g.runs + g.rows - 1) / g.rows, a.s.B * a.s.H, (g.nvec + g.nvt - 1) / g.nvt);
   E2TTT_TRACE("conv_fwd", a.st);
   auto kern = a.s.silu ? conv_fwd_kernel<T, W, VEC, true> : conv_fwd_kernel<T, W, VEC, false>;
-  kern<<<grid, g.nvt * g.rows, 0, a.st>>>(
+  const int threads = g.nvt * g.rows;
+  const size_t smem = ring_bytes<T, VEC, 1>(threads);
+  const cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, threads, smem, a.st>>>(
       g, (const T*)a.x, a.w, a.bias, (const T*)a.state, a.lengths, (T*)y, (T*)state_end);
   return cudaGetLastError();
 }
@@ -508,17 +584,20 @@ cudaError_t fwd_t(const ConvArgs& a, void* y, void* state_end) {
 template <typename T, int W, int VEC>
 cudaError_t bwd_t(const ConvArgs& a, const void* dy, const void* dstate_end, void* dx, float* dw,
                   float* dbias, void* dstate, void* ws) {
-  const Geo g = geometry(a.s, VEC);
+  const Geo g = geometry(a.s, VEC, true);
   const int gx = bwd_blocks_x(a.s, g);
   dim3 grid(gx, a.s.B * a.s.H, (g.nvec + g.nvt - 1) / g.nvt);
   const int threads = g.nvt * g.rows;
   {
     E2TTT_TRACE("conv_bwd", a.st);
     auto kern = a.s.silu ? conv_bwd_kernel<T, W, VEC, true> : conv_bwd_kernel<T, W, VEC, false>;
-    kern<<<grid, threads, threads * VEC * sizeof(float), a.st>>>(
+    const size_t smem = ring_bytes<T, VEC, 2>(threads);
+    cudaError_t e = allow_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, threads, smem, a.st>>>(
         g, (const T*)a.x, a.w, a.bias, (const T*)a.state, a.lengths, (const T*)dy,
         (const T*)dstate_end, (T*)dx, (T*)dstate, (float*)ws);
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   E2TTT_TRACE("conv_sum", a.st);
@@ -564,7 +643,7 @@ size_t conv_bwd_workspace_bytes(const ConvDims& s) {
   size_t most = 0;
   for (int vec : {1, 4}) {
     if (s.d % vec) continue;
-    const size_t n = (size_t)s.B * bwd_blocks_x(s, geometry(s, vec)) * s.H * (s.W + 1) * s.d * sizeof(float);
+    const size_t n = (size_t)s.B * bwd_blocks_x(s, geometry(s, vec, true)) * s.H * (s.W + 1) * s.d * sizeof(float);
     if (n > most) most = n;
   }
   return most;

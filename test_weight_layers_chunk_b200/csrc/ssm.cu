@@ -117,15 +117,6 @@ __device__ __forceinline__ Where where(const SsmDims& s, const int* lengths) {
   return w;
 }
 
-__device__ __forceinline__ ChunkLogs chunk_logs(float* p, int Q) {
-  ChunkLogs L;
-  L.hi = p;
-  L.lo = p + Q;
-  L.eta = p + 2 * Q;
-  L.Q1 = Q - 1;
-  return L;
-}
-
 // states[c][bh] = the chunk's own contribution to its end state
 //   REV 0: sum_s e^{c_Q-c_s} eta_s x_s y_s^T  (x = v, y = k)
 //   REV 1: sum_t e^{c_t} x_t y_t^T            (x = dy, y = q; the adjoint)
@@ -140,8 +131,8 @@ __global__ void __launch_bounds__(kT)
   const Where w = where(s, lengths);
   if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0) *status = 0;  // nothing here waits
   const int Q = s.Q, N = s.N, XP = kXP, NP = pad8(N) + 4;
-  const ChunkLogs L = chunk_logs(sm, Q);
-  float* xs = sm + 3 * Q;
+  const ChunkLogs L(sm, Q);
+  float* xs = sm + kLogRows * Q;
   float* ys = xs + Q * XP;
   if (threadIdx.x < 32) fill_chunk_logs(L, dt + (long long)w.bh * s.T + w.t0, A[w.h], w.n);
   load_tile<T>(ys, NP, y + (((long long)w.b * s.G + w.g) * s.T + w.t0) * N, N, Q, w.n, N, pad8(N));
@@ -149,10 +140,10 @@ __global__ void __launch_bounds__(kT)
   __syncthreads();
   for (int i = threadIdx.x; i < Q * kSsmPT; i += kT) {
     const int t = i / kSsmPT, p = i - t * kSsmPT;
-    xs[t * XP + p] *= REV ? L.from_start(t) : L.to_end(t) * L.eta[t];
+    xs[t * XP + p] *= REV ? L.start[t] : L.end[t] * L.eta[t];
   }
   if (threadIdx.x == 0 && w.pt == 0)
-    decay[(long long)w.c * s.B * s.H + w.bh] = L.from_start(Q - 1);
+    decay[(long long)w.c * s.B * s.H + w.bh] = L.start[Q - 1];
   __syncthreads();
   float* out = states + (((long long)w.c * s.B * s.H + w.bh) * s.P + w.p0) * N;
   for (int n0 = 0; n0 < N; n0 += 64) {
@@ -234,8 +225,8 @@ __global__ void __launch_bounds__(kT)
   extern __shared__ float sm[];
   const Where w = where(s, lengths);
   const int Q = s.Q, N = s.N, XP = kXP, NP = pad8(N) + 4, QP = Q + 4;
-  const ChunkLogs L = chunk_logs(sm, Q);
-  float* qs = sm + 3 * Q;
+  const ChunkLogs L(sm, Q);
+  float* qs = sm + kLogRows * Q;
   float* ks = qs + Q * NP;  // then the state [PT][NP]
   float* xs = ks + (Q > kSsmPT ? Q : kSsmPT) * NP;
   float* ws = xs + Q * XP;
@@ -266,7 +257,7 @@ __global__ void __launch_bounds__(kT)
 #pragma unroll
   for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc.v[j][e] *= L.from_start(acc.row() + 8 * (e >> 1));
+    for (int e = 0; e < 4; ++e) acc.v[j][e] *= L.start[acc.row() + 8 * (e >> 1)];
   acc.mm(ws, QP, 1, xs, XP, 1, Q, 0, kSsmPT - 1);
   const float Dh = D ? D[w.h] : 0.f;
   T* out = y + ((long long)w.bh * s.T + w.t0) * s.P + w.p0;
@@ -305,14 +296,14 @@ __global__ void __launch_bounds__(kT)
                       const int* __restrict__ lengths, const float* __restrict__ states,
                       const float* __restrict__ ends, const T* __restrict__ dy,
                       float* __restrict__ dqp, float* __restrict__ dkp, T* __restrict__ dv,
-                      float* __restrict__ ddtp, float* __restrict__ dAp, float* __restrict__ dDp) {
+                      float* __restrict__ ddtp, double* __restrict__ dAp, float* __restrict__ dDp) {
   extern __shared__ float sm[];
   const Where w = where(s, lengths);
   const int Q = s.Q, N = s.N, XP = kXP, NP = pad8(N) + 4, QP = Q + 4;
-  const ChunkLogs L = chunk_logs(sm, Q);
+  const ChunkLogs L(sm, Q);
   // [4][Q]: row sums of Z off its diagonal, column sums of Z / eta off it, and the
   // diagonals of Z / eta and of K
-  float* dots = sm + 3 * Q;
+  float* dots = sm + kLogRows * Q;
   float* scratch = dots + 4 * Q;
   float* qs = scratch + 16;
   float* ks = qs + Q * NP;
@@ -322,7 +313,8 @@ __global__ void __launch_bounds__(kT)
   float* gs = xs + Q * XP;
   float* Ws = gs + Q * XP;  // e^{c_t-c_s} (q_t.k_s)
   float* Ks = Ws + Q * QP;  // e^{c_t-c_s} eta_s (dy_t.v_s)
-  float* cz = Ks + Q * QP;  // [8][Q]: sums by warp
+  float* cz = Ks + Q * QP;       // [8][Q]: sums by warp
+  float* parts = cz + 8 * Q;     // [2][R / 2][Q]: rows' and columns' sums by blocks of 32
   if (threadIdx.x < 32) fill_chunk_logs(L, dt + (long long)w.bh * s.T + w.t0, A[w.h], w.n);
   const long long qo = (((long long)w.b * s.G + w.g) * s.T + w.t0) * N;
   const long long vo = ((long long)w.bh * s.T + w.t0) * s.P + w.p0;
@@ -380,9 +372,20 @@ __global__ void __launch_bounds__(kT)
   }
   __syncthreads();
   for (int u = threadIdx.x; u < Q; u += kT) {
+    // by blocks of 32 tokens (a warp's share is R * 8 columns, 16 rows), then in all
+    constexpr int K = R / 2, kAcross = Tile<R>::W / K;
     float z = 0.f, c = 0.f;
-    for (int i = 0; i < Tile<R>::W; ++i) z += cz[i * Q + u];
-    for (int i = 0; i < R; ++i) c += cz[(4 + i) * Q + u];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float zk = 0.f;
+#pragma unroll
+      for (int i = 0; i < kAcross; ++i) zk += R * 8 * (k * kAcross + i) < Q ? cz[(k * kAcross + i) * Q + u] : 0.f;
+      const float ck = cz[(4 + 2 * k) * Q + u] + cz[(5 + 2 * k) * Q + u];
+      parts[k * Q + u] = zk;
+      parts[(K + k) * Q + u] = ck;
+      z += zk;
+      c += ck;
+    }
     dots[u] = z;
     dots[Q + u] = c;
   }
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kT)
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc.v[j][e] *= L.to_end(acc.row() + 8 * (e >> 1));
+      for (int e = 0; e < 4; ++e) acc.v[j][e] *= L.end[acc.row() + 8 * (e >> 1)];
     acc.mm(Ws, 1, QP, gs, XP, 1, Q, 0, kSsmPT - 1);
     const float Dh = D ? D[w.h] : 0.f;
 #pragma unroll
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kT)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int t = acc.row() + 8 * (e >> 1), n = n0 + acc.col(j) + (e & 1);
-          const float x = acc.v[j][e] * (which ? L.to_end(t) : L.from_start(t));
+          const float x = acc.v[j][e] * (which ? L.end[t] : L.start[t]);
           dot[which][e >> 1] = fmaf(n < N ? x : 0.f, mine[t * NP + min(n, N - 1)], dot[which][e >> 1]);
           acc.v[j][e] = which ? x * L.eta[t] : x;
         }
@@ -459,6 +462,7 @@ __global__ void __launch_bounds__(kT)
     // ddt, dA, dD: lane l has the tokens l * K .. l * K + K - 1
     constexpr int K = R / 2;  // Q / 32
     const int lane = threadIdx.x;
+    double in4[K], out4[K];
     float a4[K], b4[K], src[K], as = 0.f, bs = 0.f, dD = 0.f;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
@@ -469,8 +473,10 @@ __global__ void __launch_bounds__(kT)
         rd += cz[x * Q + r];
         src[i] += cz[(4 + x) * Q + r];
       }
+      in4[i] = rd;
+      out4[i] = (double)L.eta[r] * src[i];
       a4[i] = (dots[r] - L.eta[r] * dots[Q + r]) + rd;
-      b4[i] = L.eta[r] * src[i];
+      b4[i] = (float)out4[i];
       as += a4[i];
       bs += b4[i];
       dD += dots[3 * Q + r];
@@ -487,8 +493,11 @@ __global__ void __launch_bounds__(kT)
     before = __shfl_up_sync(~0u, before, 1);
     after = lane < 31 ? after : 0.f;
     before = lane > 0 ? before : 0.f;
-    const float through = L.from_start(Q - 1) * __shfl_sync(~0u, ip, 0), Ah = A[w.h];
-    const double dA = decay_gradient<K>(a4, b4, L.eta + lane * K, through, lane);
+    ip = __shfl_sync(~0u, ip, 0);
+    const float through = L.start[Q - 1] * ip, Ah = A[w.h];
+    const double dA = decay_gradient<K>([&](int c, int i) { return parts[c * Q + lane * K + i]; },
+                                        [&](int d, int i) { return parts[(K + d) * Q + lane * K + i]; }, in4, out4,
+                                        L.eta + lane * K, (double)L.start[Q - 1] * ip, lane);
     float dl[K];
 #pragma unroll
     for (int i = K - 1; i >= 0; --i) dl[i] = after += a4[i];
@@ -505,7 +514,7 @@ __global__ void __launch_bounds__(kT)
     for (int d = 16; d; d >>= 1) dD += __shfl_xor_sync(~0u, dD, d);
     if (lane == 0) {
       const long long o = ((long long)w.c * s.NPT + w.pt) * s.B * s.H + w.bh;
-      dAp[o] = (float)dA;
+      dAp[o] = dA;
       dDp[o] = dD;
     }
   }
@@ -542,7 +551,7 @@ __device__ __forceinline__ void group_sum(const float* part, int parts, long lon
   }
 }
 // dA[h], dD[h]: sums of part [rows][H], one block per head, in a fixed order.
-__device__ void head_sum(const float* dAp, const float* dDp, int rows, int H, int h, float* dA, float* dD) {
+__device__ void head_sum(const double* dAp, const float* dDp, int rows, int H, int h, float* dA, float* dD) {
   __shared__ double s[2][kT / 32];
   double a[2] = {0.0, 0.0};
   for (int i = threadIdx.x; i < rows; i += kT) {
@@ -569,7 +578,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kT)
     grad_sums_kernel(const float* __restrict__ dqp, const float* __restrict__ dkp, int parts,
                      long long row, T* __restrict__ dq, T* __restrict__ dk,
-                     const float* __restrict__ dAp, const float* __restrict__ dDp, int rows, int H,
+                     const double* __restrict__ dAp, const float* __restrict__ dDp, int rows, int H,
                      float* __restrict__ dA, float* __restrict__ dD, int z0) {
   griddep_wait();
   const int z = blockIdx.z + z0;
@@ -675,16 +684,16 @@ __global__ void __launch_bounds__(kT)
 }
 
 size_t state_smem(const SsmDims& s) {
-  return sizeof(float) * (3 * s.Q + (size_t)s.Q * kXP + (size_t)s.Q * (pad8(s.N) + 4));
+  return sizeof(float) * (kLogRows * s.Q + (size_t)s.Q * kXP + (size_t)s.Q * (pad8(s.N) + 4));
 }
 size_t out_smem(const SsmDims& s) {
-  return sizeof(float) * (3 * s.Q + (size_t)(s.Q + (s.Q > kSsmPT ? s.Q : kSsmPT)) * (pad8(s.N) + 4) +
+  return sizeof(float) * (kLogRows * s.Q + (size_t)(s.Q + (s.Q > kSsmPT ? s.Q : kSsmPT)) * (pad8(s.N) + 4) +
                           (size_t)s.Q * kXP + (size_t)s.Q * (s.Q + 4));
 }
 size_t grad_smem(const SsmDims& s) {
-  return sizeof(float) * (7 * s.Q + 16 + (size_t)2 * (s.Q + kSsmPT) * (pad8(s.N) + 4) +
+  return sizeof(float) * ((kLogRows + 4) * s.Q + 16 + (size_t)2 * (s.Q + kSsmPT) * (pad8(s.N) + 4) +
                           (size_t)2 * s.Q * kXP + (size_t)2 * s.Q * (s.Q + 4) +
-                          (size_t)8 * s.Q);
+                          (size_t)12 * s.Q);
 }
 
 template <class F>
@@ -714,7 +723,7 @@ size_t cut_bwd(const SsmDims& s, char* ws, float* ddt, SsmBwdScratch* w) {
   w->dq = take(sums);
   w->dk = take(sums);
   w->ddt = s.NPT > 1 ? take(s.NPT * BH * s.T * f) : ddt;
-  w->dA = take((size_t)s.NC * s.NPT * BH * f);
+  w->dA = (double*)take((size_t)s.NC * s.NPT * BH * sizeof(double));
   w->dD = take((size_t)s.NC * s.NPT * BH * f);
   return o;
 }
@@ -792,7 +801,7 @@ static cudaError_t grad_sums_t(const SsmBwdArgs& a, const SsmBwdScratch& w, int 
   const dim3 grid = direct ? dim3(s.H, 1, 1) : dim3((unsigned)((row + per - 1) / per), s.B * s.G, 3);
   E2TTT_TRACE("ssm_grad_sums", a.st);
   return launch_pdl(vec ? grad_sums_kernel<T, 4> : grad_sums_kernel<T, 1>, grid, dim3(kT), 0, a.st,
-                    (const float*)w.dq, (const float*)w.dk, parts, row, (T*)a.dq, (T*)a.dk, (const float*)w.dA,
+                    (const float*)w.dq, (const float*)w.dk, parts, row, (T*)a.dq, (T*)a.dk, (const double*)w.dA,
                     (const float*)w.dD, s.NC * s.NPT * s.B, s.H, a.dA, a.dD, direct ? 2 : 0);
 }
 cudaError_t ssm_grad_sums(const SsmBwdArgs& a, const SsmBwdScratch& w, int parts) {

@@ -29,21 +29,21 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// The logarithms c_t in units of log2, each as an fp32 value and what that
-// rounding left: c reaches hundreds within a chunk, where one fp32 value would
-// be off by 1e-5 while the decay between neighbouring tokens is near one.
+// What a chunk's decays are made of, [kLogRows][Q]: the logarithms c_t in units of
+// log2, each as an fp32 value and what that rounding left (c reaches hundreds within
+// a chunk, where one fp32 value would be off by 1e-5 while the decay between
+// neighbouring tokens is near one); eta_t; and, rounded once from fp64 since the
+// states carry them along the whole row, e^{c_t}, e^{c_Q-c_t}, and e^{c_r-c_t} with r
+// the last token of t's block of 32.
+constexpr int kLogRows = 6;
 struct ChunkLogs {
-  float* hi;   // [Q]
-  float* lo;   // [Q]
-  float* eta;  // [Q]
+  float *hi, *lo, *eta, *start, *end, *tail;
+  int Q1;  // Q - 1
+  __device__ __forceinline__ ChunkLogs(float* p, int Q)
+      : hi(p), lo(p + Q), eta(p + 2 * Q), start(p + 3 * Q), end(p + 4 * Q), tail(p + 5 * Q), Q1(Q - 1) {}
   __device__ __forceinline__ float decay(int t, int s) const {  // e^{c_t - c_s}
     return ex2((hi[t] - hi[s]) + (lo[t] - lo[s]));
   }
-  __device__ __forceinline__ float from_start(int t) const { return ex2(hi[t] + lo[t]); }
-  __device__ __forceinline__ float to_end(int s) const {
-    return ex2((hi[Q1] - hi[s]) + (lo[Q1] - lo[s]));
-  }
-  int Q1;  // Q - 1
 };
 
 // One warp fills the logs of a chunk of Q <= 128 tokens (a multiple of 32), of
@@ -69,6 +69,7 @@ __device__ __forceinline__ void fill_chunk_logs(const ChunkLogs& L, const float*
     const double u = __shfl_up_sync(~0u, pre, o);
     if (lane >= o) pre += u;
   }
+  const double last = __shfl_sync(~0u, pre, 31), block = __shfl_sync(~0u, pre, lane | (32 / per - 1));
   pre -= sum;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -78,19 +79,29 @@ __device__ __forceinline__ void fill_chunk_logs(const ChunkLogs& L, const float*
       const float h = (float)c;
       L.hi[t] = h;
       L.lo[t] = (float)(c - (double)h);
+      L.start[t] = (float)exp2(c);
+      L.end[t] = (float)exp2(last - c);
+      L.tail[t] = (float)exp2(block - c);
     }
   }
 }
 
 // A chunk's part of dA = sum_r eta_r dl_r, by one warp (lane l has the tokens l K ..
-// l K + K - 1), with dl_r = sum_{t>=r} a_t + sum_{s<r} b_s + through. Summed the
-// other way round, with E_t = eta_1 + .. + eta_t, it is
-//   sum_t a_t E_t + sum_s b_s (E_Q - E_s) + through E_Q,
-// in fp64: the chunks' parts cancel to a few hundredths of their size.
-template <int K>
-__device__ __forceinline__ double decay_gradient(const float (&a)[K], const float (&b)[K], const float* eta,
-                                                 float through, int lane) {
-  double E[K], run = 0.0;
+// l K + K - 1, K = Q / 32). Summed by what passes over r instead, with E_t = eta_1 +
+// .. + eta_t, it is
+//   sum_{s<t} Z_ts (E_t - E_s) + sum_t in_t E_t + sum_s out_s (E_Q - E_s) + through E_Q
+// (in, out: the terms of readers and of sources beside the chunk's own pairs). The
+// pairs come as sums over blocks of 32 tokens, rows(c, t) over the sources in block
+// c and cols(d, s) over the readers in block d: with E counted from the end of an
+// earlier block, or within one from its start, little of them cancels. In fp64, as
+// the chunks' parts cancel to a few hundredths of their size.
+template <int K, class Rows, class Cols>
+__device__ __forceinline__ double decay_gradient(Rows rows, Cols cols, const double (&in)[K],
+                                                 const double (&out)[K], const float* eta, double through,
+                                                 int lane) {
+  constexpr int kLanes = 32 / K;  // lanes of a block
+  const int mine = lane / kLanes;
+  double E[K], run = 0.0, ends[K];
 #pragma unroll
   for (int i = 0; i < K; ++i) E[i] = run += eta[i];
   double pre = run;
@@ -99,11 +110,26 @@ __device__ __forceinline__ double decay_gradient(const float (&a)[K], const floa
     const double u = __shfl_up_sync(~0u, pre, o);
     pre += lane >= o ? u : 0.0;
   }
-  const double all = __shfl_sync(~0u, pre, 31);
-  pre -= run;
-  double sum = lane == 0 ? through * all : 0.0;
 #pragma unroll
-  for (int i = 0; i < K; ++i) sum += a[i] * (pre + E[i]) + b[i] * (all - (pre + E[i]));
+  for (int c = 0; c < K; ++c) ends[c] = __shfl_sync(~0u, pre, (c + 1) * kLanes - 1);
+  pre -= run;
+  double first = 0.0, last = 0.0;
+#pragma unroll
+  for (int c = 0; c < K; ++c) {
+    first = c + 1 == mine ? ends[c] : first;
+    last = c == mine ? ends[c] : last;
+  }
+  double sum = lane == 0 ? through * ends[K - 1] : 0.0;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const double e = pre + E[i];
+    sum += in[i] * e + out[i] * (ends[K - 1] - e);
+#pragma unroll
+    for (int c = 0; c < K; ++c) {
+      if (c <= mine) sum += (double)rows(c, i) * (e - (c < mine ? ends[c] : first));
+      if (c >= mine) sum += (double)eta[i] * cols(c, i) * (c > mine ? last - e : first - e);
+    }
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   return sum;

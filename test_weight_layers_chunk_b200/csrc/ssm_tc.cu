@@ -170,20 +170,9 @@ __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
   }
 }
 
-// Per chunk in global memory, written once per call by logs_kernel: [3][kQ] hi,
-// lo and eta of its tokens (see ChunkLogs).
-struct __align__(16) Logs {
-  float hi[kQ], lo[kQ], eta[kQ];
-};
-
-__device__ __forceinline__ ChunkLogs logs_view(float* p) {
-  ChunkLogs L;
-  L.hi = p;
-  L.lo = p + kQ;
-  L.eta = p + 2 * kQ;
-  L.Q1 = kQ - 1;
-  return L;
-}
+// Floats of a chunk's logs, which logs_kernel writes once per call to
+// [B*H][NC][kLogRows][kQ].
+constexpr int kLogs = kLogRows * kQ;
 
 // One warp per (batch row, head, chunk): its logs and decay e^{c_Q}; resets the
 // status word of the launches that follow.
@@ -191,27 +180,27 @@ __global__ void __launch_bounds__(128)
     logs_kernel(SsmDims s, const float* __restrict__ dt, const float* __restrict__ A,
                 const int* __restrict__ lengths, float* __restrict__ logs,
                 float* __restrict__ decay, int* __restrict__ status) {
-  __shared__ Logs sm[4];
+  __shared__ __align__(16) float sm[4][kLogs];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 4 + w, bh = blockIdx.y, b = bh / s.H;
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x == 0 && bh == 0 && threadIdx.x == 0) *status = 0;
   if (c >= s.NC) return;
-  const ChunkLogs L = logs_view(sm[w].hi);
+  const ChunkLogs L(sm[w], kQ);
   const int t0 = c * kQ;
   fill_chunk_logs(L, dt + (long long)bh * s.T + t0, A[bh - b * s.H],
                   min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ));
   __syncwarp();
-  float4* out = reinterpret_cast<float4*>(logs + ((long long)bh * s.NC + c) * 3 * kQ);
+  float4* out = reinterpret_cast<float4*>(logs + ((long long)bh * s.NC + c) * kLogs);
 #pragma unroll
-  for (int i = 0; i < 3; ++i) out[i * 32 + lane] = reinterpret_cast<const float4*>(sm[w].hi)[i * 32 + lane];
-  if (lane == 0) decay[(long long)c * s.B * s.H + bh] = L.from_start(kQ - 1);
+  for (int i = 0; i < kLogRows; ++i) out[i * 32 + lane] = reinterpret_cast<const float4*>(sm[w])[i * 32 + lane];
+  if (lane == 0) decay[(long long)c * s.B * s.H + bh] = L.start[kQ - 1];
 }
 
 __device__ __forceinline__ void load_logs(const ChunkLogs& L, const float* logs, int bh, int NC, int c) {
-  const float4* p = reinterpret_cast<const float4*>(logs + ((long long)bh * NC + c) * 3 * kQ);
-  if (threadIdx.x < 3 * kQ / 4) reinterpret_cast<float4*>(L.hi)[threadIdx.x] = p[threadIdx.x];
+  const float4* p = reinterpret_cast<const float4*>(logs + ((long long)bh * NC + c) * kLogs);
+  if (threadIdx.x < kLogs / 4) reinterpret_cast<float4*>(L.hi)[threadIdx.x] = p[threadIdx.x];
 }
 
 // Set-up and tear-down that every kernel shares: an mbarrier and `COLS` columns
@@ -400,26 +389,20 @@ __global__ void __launch_bounds__(kStateStreams * kHalf, 1)
   if (threadIdx.x < kThreads)
     load_rows<kQ, 2, VEC>(ys, y + (((long long)m.b * s.G + m.g) * s.T + m.t0) * s.N, s.N, m.n, s.N);
   uint4 xv[4];
-  float hi = 0.f, lo = 0.f, eta = 0.f, end_hi = 0.f, end_lo = 0.f;
-  // This thread's row of the item, and its token's logs.
+  float w = 0.f;
+  // This thread's row of the item, and its token's weight.
   auto fetch = [&](int it) {
     const int h = m.head(it), p0 = m.first_row(it), bh = m.b * s.H + h;
     const int np = min(kPT, s.P - p0);
     const bf16* xr = x + ((long long)bh * s.T + m.t0 + t) * s.P + p0;
-    const float* lg = logs + ((long long)bh * s.NC + m.c) * 3 * kQ;
+    const float* lg = logs + ((long long)bh * s.NC + m.c) * kLogs + t;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int col = half * 32 + j * 8;
       xv[j] = uint4{0, 0, 0, 0};
       if (t < m.n && col < np) xv[j] = VEC ? *reinterpret_cast<const uint4*>(xr + col) : load8(xr, col, np);
     }
-    hi = lg[t];
-    lo = lg[kQ + t];
-    if (!REV) {
-      eta = lg[2 * kQ + t];
-      end_hi = lg[kQ - 1];
-      end_lo = lg[2 * kQ - 1];
-    }
+    w = REV ? lg[3 * kQ] : lg[4 * kQ] * lg[2 * kQ];
   };
   int it = m.i0 + wg;
   if (it < m.i1) fetch(it);
@@ -428,7 +411,6 @@ __global__ void __launch_bounds__(kStateStreams * kHalf, 1)
   GroupMmas done{&gbar[wg], 0u, status, wg};
 #pragma unroll 1
   for (; it < m.i1; it += kStateStreams) {
-    const float w = REV ? ex2(hi + lo) : ex2((end_hi - hi) + (end_lo - lo)) * eta;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t* u = &xv[j].x;
@@ -494,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const bf16* __restrict__ states, bf16* __restrict__ y, int per,
                int* __restrict__ status, const __grid_constant__ OutMaps maps) {
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(16) float slog[2][3 * kQ], stail[2][kQ], own[kQ];
+  __shared__ __align__(16) float slog[2][kLogs], own[kQ];
   __shared__ uint64_t bar, gbar[2], sbar[2], full[2];
   __shared__ uint32_t slot;
   const int wg = threadIdx.x / kHalf, t = threadIdx.x % kQ, half = threadIdx.x / kQ & 1, quad = t >> 5;
@@ -517,12 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long qo = (((long long)m.b * s.G + m.g) * s.T + m.t0) * s.N;
   load_rows<kQ, NB, VEC>(qs, q + qo, s.N, m.n, s.N);
   load_rows<kQ, NB, VEC>(ks, k + qo, s.N, m.n, s.N);
-  float hi = 0.f, lo = 0.f, eta = 0.f;
+  float hi = 0.f, lo = 0.f, eta = 0.f, start = 0.f, tail = 0.f;
   auto fetch_logs = [&](int it) {
-    const float* lg = logs + ((long long)(m.b * s.H + m.head(it)) * s.NC + m.c) * 3 * kQ;
-    hi = lg[t];
-    lo = lg[kQ + t];
-    eta = lg[2 * kQ + t];
+    const float* lg = logs + ((long long)(m.b * s.H + m.head(it)) * s.NC + m.c) * kLogs + t;
+    hi = lg[0];
+    lo = lg[kQ];
+    eta = lg[2 * kQ];
+    start = lg[3 * kQ];
+    tail = lg[5 * kQ];
   };
   // An item's state and rows: by TMA where a row of the tile is either a token that
   // exists or beyond T (which reads as zero), else by the group's threads.
@@ -581,8 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(Ws + piece<kQ>(t, cb * 4 + i)) = uint4{0, 0, 0, 0};
     GroupMmas done{&gbar[wg], 0u, status, wg};
-    const ChunkLogs L = logs_view(slog[wg]);
-    float* tail = stail[wg];
+    const ChunkLogs L(slog[wg], kQ);  // tail here with eta
     int buf = 0;
     uint32_t phase = 0;  // of the loads and of the state's product
     bool lead_ok = true, gave_up = false;
@@ -590,14 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; it < m.i1; it += 2, buf ^= 1) {
       const int h = m.head(it), p0 = m.first_row(it), bh = m.b * s.H + h;
       const int np = min(kPT, s.P - p0);
-      const float tl = ex2((__shfl_sync(~0u, hi, 31) - hi) + (__shfl_sync(~0u, lo, 31) - lo)) * eta;
       if (half == 0) {
         L.hi[t] = hi;
         L.lo[t] = lo;
         L.eta[t] = eta;
-        tail[t] = tl;
+        L.tail[t] = tail * eta;
       }
-      const float f = ex2(hi + lo), thi = hi, tlo = lo;
+      const float f = start, thi = hi, tlo = lo;
       cp_wait();
       group_publish(wg);  // the item's logs, and what the threads loaded, are there
       if (leader) {
@@ -618,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 o[4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 w = *reinterpret_cast<const float4*>(tail + cb * 32 + i * 4);
+          const float4 w = *reinterpret_cast<const float4*>(L.tail + cb * 32 + i * 4);
           uint32_t* ow = &o[i >> 1].x + (i & 1) * 2;
           ow[0] = pack2(a[i * 4] * (row * w.x), a[i * 4 + 1] * (row * w.y));
           ow[1] = pack2(a[i * 4 + 2] * (row * w.z), a[i * 4 + 3] * (row * w.w));
@@ -717,12 +699,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   block_end<512>(tmem);
 }
 
-// The decays' second factors, for the gradients: e^{c_r - c_s} with r the last
-// token of s's block of 32.
-__device__ __forceinline__ void fill_tails(const ChunkLogs& L, float* tail) {
-  if (threadIdx.x < kQ) tail[threadIdx.x] = L.decay(threadIdx.x | 31, threadIdx.x);
-}
-
 // ------------------------------------------------------------------ gradients
 // 16 columns of one value per (row = lane, column): the sum over the warp's
 // lanes of column `lane & 15`, to that lane.
@@ -742,7 +718,9 @@ struct GradOut {
   float *dq, *dk;    // [B*G][parts][T][N]: sums over a part's heads, fp32
   bf16 *dq16, *dk16; // the results themselves, where there is one part
   bf16* dv;
-  float *ddt, *dA, *dD;
+  float* ddt;
+  double* dA;
+  float* dD;
 };
 
 // All gradients of one chunk for a run of heads of one group (and their tiles of
@@ -767,8 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int per, int* __restrict__ status) {
   constexpr int kTerm = NB * kPT * 128;  // bytes of one term of a state
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(16) float slog[3 * kQ];
-  __shared__ __align__(16) float tail[kQ];
+  __shared__ __align__(16) float slog[kLogs];
   __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[3][kQ],
       warp_ip[kThreads / 32];
   __shared__ uint64_t bar;
@@ -783,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* St = W1;                  // S, three terms, and X's second and third, under W1 and W2
   const int c = blockIdx.x, bg = blockIdx.y, b = bg / s.G, g = bg - b * s.G, split = blockIdx.z;
   const int HG = s.H / s.G, items = HG * s.NPT, BH = s.B * s.H, t0 = c * kQ;
-  const ChunkLogs L = logs_view(slog);
+  const ChunkLogs L(slog, kQ);
   const uint32_t tmem = block_begin<512>(&bar, &slot);
   griddep_wait();
   griddep_launch_dependents();
@@ -864,11 +841,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, Xs, kPT / 16, true);
       tc::mma_commit(&bar);
     }
-    fill_tails(L, tail);
     if (!(ok = done.wait())) break;
     // the states' parts of dq and dk, and their dots with q and k
     {
-      const float f = L.from_start(t), e = L.to_end(t), ee = e * L.eta[t];
+      const float f = L.start[t], e = L.end[t], ee = e * L.eta[t];
       const bool add = it > i0;
       float rd = 0.f, sd = 0.f;
 #pragma unroll
@@ -931,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float row = L.decay(t, part * 32 + 31);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 v4 = *reinterpret_cast<const float4*>(tail + u0 + i * 4);
+            const float4 v4 = *reinterpret_cast<const float4*>(L.tail + u0 + i * 4);
             e[i * 4] = row * v4.x, e[i * 4 + 1] = row * v4.y, e[i * 4 + 2] = row * v4.z, e[i * 4 + 3] = row * v4.w;
           }
         } else {
@@ -1005,63 +981,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mma_commit(&bar);
     }
     if (it + 1 < i1) fetch_states(it + 1);
-    if (warp == kThreads / 32 - 1) {
-      // ddt, dA, dD: lane l has the tokens 4 l .. 4 l + 3
-      float a4[4], b4[4], off4[4], src4[4], as = 0.f, bs = 0.f, dsum = 0.f;
+    if (warp >= kThreads / 32 - 2) {
+      // Two warps make ddt, and dA and dD, while the MMAs run: lane l has the tokens
+      // 4 l .. 4 l + 3.
+      const bool for_dt = warp == kThreads / 32 - 1;
       float ip = lane < kThreads / 32 ? warp_ip[lane] : 0.f;
 #pragma unroll
       for (int d = kThreads / 64; d; d >>= 1) ip += __shfl_xor_sync(~0u, ip, d);
       ip = __shfl_sync(~0u, ip, 0);
+      float in4[4], src4[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = lane * 4 + i;
-        float off = 0.f;
-#pragma unroll
-        for (int qd = 0; qd < 4; ++qd) off += qd >= r >> 5 ? cols[qd][r] : 0.f;
-        off4[i] = off;
+        in4[i] = (rdr[0][r] + rdr[1][r]) + (rdr[2][r] + rdr[3][r]);
         src4[i] = (src[0][r] + src[1][r]) + (src[2][r] + src[3][r]);
-        a4[i] = ((rows[0][r] + rows[1][r]) + (rows[2][r] + rows[3][r]) - L.eta[r] * off) +
-                ((rdr[0][r] + rdr[1][r]) + (rdr[2][r] + rdr[3][r]));
-        b4[i] = L.eta[r] * src4[i];
-        as += a4[i];
-        bs += b4[i];
-        dsum += diag[1][r];
       }
-      float after = as, before = bs;  // of this lane's tokens on; up to them
+      if (for_dt) {
+        float a4[4], b4[4], off4[4], as = 0.f, bs = 0.f;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const float x = __shfl_down_sync(~0u, after, d), y = __shfl_up_sync(~0u, before, d);
-        after += lane + d < 32 ? x : 0.f;
-        before += lane >= d ? y : 0.f;
-      }
-      // exclusive of this lane's own, without taking them off again
-      after = __shfl_down_sync(~0u, after, 1);
-      before = __shfl_up_sync(~0u, before, 1);
-      after = lane < 31 ? after : 0.f;
-      before = lane > 0 ? before : 0.f;
-      const float through = L.from_start(kQ - 1) * ip, Ah = A[h];
-      const double dA = decay_gradient<4>(a4, b4, L.eta + lane * 4, through, lane);
-      float dl[4];
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane * 4 + i;
+          float off = 0.f;
 #pragma unroll
-      for (int i = 3; i >= 0; --i) dl[i] = after += a4[i];
+          for (int qd = 0; qd < 4; ++qd) off += qd >= r >> 5 ? cols[qd][r] : 0.f;
+          off4[i] = off;
+          a4[i] = ((rows[0][r] + rows[1][r]) + (rows[2][r] + rows[3][r]) - L.eta[r] * off) + in4[i];
+          b4[i] = L.eta[r] * src4[i];
+          as += a4[i];
+          bs += b4[i];
+        }
+        float after = as, before = bs;  // of this lane's tokens on; up to them
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dl[i] += before + through;
-        before += b4[i];
-      }
-      float* out = o.ddt + ((long long)pt * BH + bh) * s.T + t0;
+        for (int d = 1; d < 32; d <<= 1) {
+          const float x = __shfl_down_sync(~0u, after, d), y = __shfl_up_sync(~0u, before, d);
+          after += lane + d < 32 ? x : 0.f;
+          before += lane >= d ? y : 0.f;
+        }
+        // exclusive of this lane's own, without taking them off again
+        after = __shfl_down_sync(~0u, after, 1);
+        before = __shfl_up_sync(~0u, before, 1);
+        after = lane < 31 ? after : 0.f;
+        before = lane > 0 ? before : 0.f;
+        const float through = L.start[kQ - 1] * ip, Ah = A[h];
+        float dl[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = lane * 4 + i;
-        const float x = fmaf(Ah, dl[i], off4[i] + diag[0][r] + src4[i]);
-        if (t0 + r < s.T) out[r] = r < n ? x : 0.f;
-      }
+        for (int i = 3; i >= 0; --i) dl[i] = after += a4[i];
+        float* out = o.ddt + ((long long)pt * BH + bh) * s.T + t0;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) dsum += __shfl_xor_sync(~0u, dsum, d);
-      if (lane == 0) {
-        const long long at = ((long long)c * s.NPT + pt) * BH + bh;
-        o.dA[at] = (float)dA;
-        o.dD[at] = dsum;
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane * 4 + i;
+          dl[i] += before + through;
+          before += b4[i];
+          const float x = fmaf(Ah, dl[i], off4[i] + diag[0][r] + src4[i]);
+          if (t0 + r < s.T) out[r] = r < n ? x : 0.f;
+        }
+      } else {
+        double in[4], out[4];
+        float dsum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane * 4 + i;
+          in[i] = in4[i];
+          out[i] = (double)L.eta[r] * src4[i];
+          dsum += diag[1][r];
+        }
+        const double dA = decay_gradient<4>([&](int cb, int i) { return rows[cb][lane * 4 + i]; },
+                                            [&](int qd, int i) { return cols[qd][lane * 4 + i]; }, in, out,
+                                            L.eta + lane * 4, (double)L.start[kQ - 1] * ip, lane);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) dsum += __shfl_xor_sync(~0u, dsum, d);
+        if (lane == 0) {
+          const long long at = ((long long)c * s.NPT + pt) * BH + bh;
+          o.dA[at] = dA;
+          o.dD[at] = dsum;
+        }
       }
       __syncwarp();
     }
@@ -1070,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ld[2][16];
       tmem_ld16<2>({lanes + part * 16, lanes + 64 + part * 16}, ld);
       float(&a1)[16] = ld[0], (&a2)[16] = ld[1];
-      const float e = L.to_end(t), eta = L.eta[t], Dh = fmaf(eta, diag[2][t], D ? D[h] : 0.f);
+      const float e = L.end[t], eta = L.eta[t], Dh = fmaf(eta, diag[2][t], D ? D[h] : 0.f);
       bf16* out = o.dv + vo + (long long)t * s.P + part * 16;
       if (t0 + t < s.T)
 #pragma unroll
@@ -1215,7 +1208,7 @@ bool vectors(const SsmDims& s, std::initializer_list<const void*> ps) {
 }  // namespace
 
 size_t ssm_tc_logs_bytes(const SsmDims& s) {
-  return (size_t)s.B * s.H * s.NC * 3 * kQ * sizeof(float);
+  return (size_t)s.B * s.H * s.NC * kLogs * sizeof(float);
 }
 
 int ssm_tc_grad_parts(const SsmDims& s) { return grad_parts(s); }

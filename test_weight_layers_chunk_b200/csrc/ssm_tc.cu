@@ -174,28 +174,44 @@ __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
 // [B*H][NC][kLogRows][kQ].
 constexpr int kLogs = kLogRows * kQ;
 
-// One warp per (batch row, head, chunk): its logs and decay e^{c_Q}; resets the
-// status word of the launches that follow.
-__global__ void __launch_bounds__(128)
+// One block per (chunk, batch row and head), one thread per token: its logs (see
+// ChunkLogs) and the chunk's decay e^{c_Q}; resets the status word of the launches
+// that follow.
+__global__ void __launch_bounds__(kQ)
     logs_kernel(SsmDims s, const float* __restrict__ dt, const float* __restrict__ A,
                 const int* __restrict__ lengths, float* __restrict__ logs,
                 float* __restrict__ decay, int* __restrict__ status) {
-  __shared__ __align__(16) float sm[4][kLogs];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 4 + w, bh = blockIdx.y, b = bh / s.H;
+  __shared__ double sums[kQ / 32];
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31, c = blockIdx.x, bh = blockIdx.y, b = bh / s.H;
   griddep_wait();
   griddep_launch_dependents();
-  if (blockIdx.x == 0 && bh == 0 && threadIdx.x == 0) *status = 0;
-  if (c >= s.NC) return;
-  const ChunkLogs L(sm[w], kQ);
-  const int t0 = c * kQ;
-  fill_chunk_logs(L, dt + (long long)bh * s.T + t0, A[bh - b * s.H],
-                  min(max(ssm_row_length(lengths, b, s.T) - t0, 0), kQ));
-  __syncwarp();
-  float4* out = reinterpret_cast<float4*>(logs + ((long long)bh * s.NC + c) * kLogs);
+  if (c == 0 && bh == 0 && t == 0) *status = 0;
+  const int n = min(max(ssm_row_length(lengths, b, s.T) - c * kQ, 0), kQ);
+  const float eta = t < n ? dt[(long long)bh * s.T + c * kQ + t] : 0.f;
+  double x = eta * ((double)A[bh - b * s.H] * 1.4426950408889634);
 #pragma unroll
-  for (int i = 0; i < kLogRows; ++i) out[i * 32 + lane] = reinterpret_cast<const float4*>(sm[w])[i * 32 + lane];
-  if (lane == 0) decay[(long long)c * s.B * s.H + bh] = L.start[kQ - 1];
+  for (int o = 1; o < 32; o <<= 1) {
+    const double u = __shfl_up_sync(~0u, x, o);
+    x += lane >= o ? u : 0.0;
+  }
+  if (lane == 31) sums[w] = x;
+  __syncthreads();
+  double before = 0.0, all = 0.0;
+#pragma unroll
+  for (int i = 0; i < kQ / 32; ++i) {
+    before += i < w ? sums[i] : 0.0;
+    all += sums[i];
+  }
+  x += before;
+  const float hi = (float)x;
+  float* out = logs + ((long long)bh * s.NC + c) * kLogs + t;
+  out[0] = hi;
+  out[kQ] = (float)(x - (double)hi);
+  out[2 * kQ] = eta;
+  out[3 * kQ] = (float)exp2(x);
+  out[4 * kQ] = (float)exp2(all - x);
+  out[5 * kQ] = (float)exp2(before + sums[w] - x);
+  if (t == 0) decay[(long long)c * s.B * s.H + bh] = (float)exp2(all);
 }
 
 __device__ __forceinline__ void load_logs(const ChunkLogs& L, const float* logs, int bh, int NC, int c) {
@@ -1221,7 +1237,7 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
   cudaError_t e;
   {
     E2TTT_TRACE("ssm_logs", a.st);
-    e = launch_pdl(logs_kernel, dim3((s.NC + 3) / 4, BH), dim3(128), 0, a.st, s, a.dt, a.A, a.lengths, w.logs,
+    e = launch_pdl(logs_kernel, dim3(s.NC, BH), dim3(kQ), 0, a.st, s, a.dt, a.A, a.lengths, w.logs,
                    w.decay, w.status);
     if (e != cudaSuccess) return e;
   }
@@ -1259,7 +1275,7 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
   cudaError_t e;
   {
     E2TTT_TRACE("ssm_logs", a.st);
-    e = launch_pdl(logs_kernel, dim3((s.NC + 3) / 4, BH), dim3(128), 0, a.st, s, a.dt, a.A, a.lengths, a.logs,
+    e = launch_pdl(logs_kernel, dim3(s.NC, BH), dim3(kQ), 0, a.st, s, a.dt, a.A, a.lengths, a.logs,
                    a.decay, a.status);
     if (e != cudaSuccess) return e;
   }

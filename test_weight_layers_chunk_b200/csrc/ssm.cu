@@ -181,35 +181,50 @@ __global__ void __launch_bounds__(kT)
     carry_kernel(int NC, int BH, long long PN, const V* __restrict__ first,
                  const float* __restrict__ decay, V* __restrict__ states, V* __restrict__ last,
                  bf16* __restrict__ copy, bool keep) {
-  constexpr int W = sizeof(V) / sizeof(float);
+  constexpr int W = sizeof(V) / sizeof(float), U = kCarryBatch;
   const int bh = blockIdx.y;
   const long long i = (long long)blockIdx.x * kT + threadIdx.x;
   griddep_wait();
   griddep_launch_dependents();
   if (i >= PN) return;
   V run = first ? first[bh * PN + i] : V{};
-  constexpr int U = kCarryBatch;
-  for (int c0 = 0; c0 < NC; c0 += U) {
+  // this element in the first chunk of the walk, and the way to the next one
+  const long long step = (REV ? -1 : 1) * (long long)BH * PN, start = (REV ? NC - 1LL : 0) * BH;
+  V* p = states + (start + bh) * PN + i;
+  bf16* to = copy ? copy + ((start + bh) * PN + i) * W : nullptr;
+  const float* d = decay + start + bh;
+  const int dstep = REV ? -BH : BH;
+  int c = 0;
+  for (; c + U <= NC; c += U) {
     V own[U];
-    float d[U];
+    float e[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
-      if (c0 + u < NC) {
-        own[u] = __ldcs(states + ((long long)c * BH + bh) * PN + i);
-        d[u] = decay[(long long)c * BH + bh];
-      }
+      own[u] = __ldcs(p + u * step);
+      e[u] = d[u * (long long)dstep];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = REV ? NC - 1 - (c0 + u) : c0 + u;
-      if (c0 + u < NC) {
-        const long long at = ((long long)c * BH + bh) * PN + i;
-        if (keep) __stcs(states + at, run);
-        if (copy) store_bf16(copy + at * W, run);
-        decay_add(run, d[u], own[u]);
+      if (keep) __stcs(p, run);
+      if (to) {
+        store_bf16(to, run);
+        to += step * W;
       }
+      decay_add(run, e[u], own[u]);
+      p += step;
+      d += dstep;
     }
+  }
+  for (; c < NC; ++c) {
+    const V own = *p;
+    if (keep) __stcs(p, run);
+    if (to) {
+      store_bf16(to, run);
+      to += step * W;
+    }
+    decay_add(run, *d, own);
+    p += step;
+    d += dstep;
   }
   if (last) last[bh * PN + i] = run;
 }

@@ -29,11 +29,32 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// 2^x to about one unit of fp32, for an exponent in fp64: 2^x = 2^n e^{f ln 2} with n
+// the nearest whole number and |f| <= 1/2, by the exponential series to the eighth
+// power (what is left out is below 2e-10).
+__device__ __forceinline__ float exp2_rounded(double x) {
+  x = fmin(fmax(x, -200.0), 200.0);  // 2^x is zero or infinite beyond
+  const double n = rint(x);
+  const float f = (float)(x - n) * 0.69314718055994531f;
+  float p = 1.0f / 40320.0f;
+  p = fmaf(p, f, 1.0f / 5040.0f);
+  p = fmaf(p, f, 1.0f / 720.0f);
+  p = fmaf(p, f, 1.0f / 120.0f);
+  p = fmaf(p, f, 1.0f / 24.0f);
+  p = fmaf(p, f, 1.0f / 6.0f);
+  p = fmaf(p, f, 0.5f);
+  p = fmaf(p, f, 1.0f);
+  p = fmaf(p, f, 1.0f);
+  // the exponent in two halves, each within range
+  const int e = (int)n, h = e / 2;
+  return p * __int_as_float((h + 127) << 23) * __int_as_float((e - h + 127) << 23);
+}
+
 // What a chunk's decays are made of, [kLogRows][Q]: the logarithms c_t in units of
 // log2, each as an fp32 value and what that rounding left (c reaches hundreds within
 // a chunk, where one fp32 value would be off by 1e-5 while the decay between
-// neighbouring tokens is near one); eta_t; and, rounded once from fp64 since the
-// states carry them along the whole row, e^{c_t}, e^{c_Q-c_t}, and e^{c_r-c_t} with r
+// neighbouring tokens is near one); eta_t; and, computed from fp64 logarithms since
+// the states carry them along the whole row, e^{c_t}, e^{c_Q-c_t}, and e^{c_r-c_t} with r
 // the last token of t's block of 32.
 constexpr int kLogRows = 6;
 struct ChunkLogs {
@@ -79,9 +100,9 @@ __device__ __forceinline__ void fill_chunk_logs(const ChunkLogs& L, const float*
       const float h = (float)c;
       L.hi[t] = h;
       L.lo[t] = (float)(c - (double)h);
-      L.start[t] = (float)exp2(c);
-      L.end[t] = (float)exp2(last - c);
-      L.tail[t] = (float)exp2(block - c);
+      L.start[t] = exp2_rounded(c);
+      L.end[t] = exp2_rounded(last - c);
+      L.tail[t] = exp2_rounded(block - c);
     }
   }
 }

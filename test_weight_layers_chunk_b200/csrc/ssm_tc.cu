@@ -383,6 +383,9 @@ __device__ __forceinline__ Items block_items(const SsmDims& s, const int* length
 // the tensor cores: y contracted over its rows (128 state columns as rows of the
 // tile), against the three terms of w x side by side, so that y is read once for
 // all three (N = 192: 80 cycles of shared-memory reads a step instead of 144).
+// 33 us for 128 heads x 2048 tokens (64 x 128 states), where its bytes take 15: a
+// chain of short steps in two streams. Results gathered in shared memory for one
+// bulk copy took 41 us, three streams with one accumulator 35.
 template <int REV, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     state_kernel(SsmDims s, const bf16* __restrict__ x, const bf16* __restrict__ y,
@@ -478,6 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // that are both at most one for a decaying state), so that only a quarter of the
 // decays takes an exponential each. A token's own term, W_tt v_t, joins D v_t in
 // fp32 instead: where it is most of y_t, y_t then has no rounding but its last.
+// 32 us for 128 heads x 2048 tokens (64 x 128 states; its bytes take 16); with a
+// chunk's q k^T made again for every head and loads by all threads it was 72.
 struct OutMaps {
   CUtensorMap v, y, S;  // [B*H][T][P] (boxes of 128 x 64), and [NC*B*H][P][N] (64 x 64)
 };
@@ -748,6 +753,10 @@ struct GradOut {
 //   three terms, later overwritten by the two score matrices (X's first term stays)
 // What the next item reads comes in under this one: its S and X to registers once
 // the last products are issued, its v and dy once the scores are made.
+// 200 us for 128 heads x 2048 tokens (64 x 128 states), some 20000 cycles an item, of
+// which the MMAs are 4100: one chain of steps, since a second stream's tiles do not
+// fit. v, dy and dv by TMA took 218 us (more registers spilled), 256 threads with dq
+// and dk in registers 268.
 template <int NB, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     grad_kernel(SsmDims s, const bf16* __restrict__ q, const bf16* __restrict__ k,

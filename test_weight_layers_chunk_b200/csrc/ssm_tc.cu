@@ -753,7 +753,7 @@ struct GradOut {
 //   three terms, later overwritten by the two score matrices (X's first term stays)
 // What the next item reads comes in under this one: its S and X to registers once
 // the last products are issued, its v and dy once the scores are made.
-// 200 us for 128 heads x 2048 tokens (64 x 128 states), some 20000 cycles an item, of
+// 207 us for 128 heads x 2048 tokens (64 x 128 states), some 20000 cycles an item, of
 // which the MMAs are 4100: one chain of steps, since a second stream's tiles do not
 // fit. v, dy and dv by TMA took 218 us (more registers spilled), 256 threads with dq
 // and dk in registers 268.
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTerm = NB * kPT * 128;  // bytes of one term of a state
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[kLogs];
-  __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[3][kQ],
+  __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[3][kQ], owned[kQ],
       warp_ip[kThreads / 32];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
@@ -799,6 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nsteps = (s.N + 15) / 16;
   Mmas done{&bar, 0u, status};
   bool ok = true;
+  if (part == quad) owned[t] = 0.f;  // sum over the items of eta_t dy_t.v_t, by the row's diagonal block's thread
 
   const int i0 = split * per, i1 = min(items, i0 + per);
   auto head = [&](int it) { return g * HG + (s.NPT == 1 ? it : it / s.NPT); };
@@ -966,6 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool on = u0 + i == t;
             dr = on ? off[i] : dr;
             dd = on ? kk[i] : dd;
+            kk[i] = on ? 0.f : kk[i];  // joins dq and dk in fp32, at the end
             m[i] = on ? 0.f : m[i];  // joins D in fp32
             off[i] = on ? 0.f : off[i];
           }
@@ -992,6 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (part == quad) {  // the quarter that holds this row's diagonal block
       diag[0][t] = dr;
       diag[1][t] = dd;
+      owned[t] = fmaf(dd, L.eta[t], owned[t]);
       if (it == i0) diag[2][t] = dm;
     }
     publish();
@@ -1109,8 +1112,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();  // the item's tiles, logs and sums are free for the next one
     tc::tc_fence_after();
   }
+  // A token's own terms, eta_t (dy_t.v_t) k_t and q_t, are added in fp32.
+  __syncthreads();
   if (ok) {
     const int parts = gridDim.z;
+    const float own = owned[t];
     const bool there = t0 + t < s.T;
 #pragma unroll
     for (int which = 0; which < 2; ++which)
@@ -1120,8 +1126,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16<1>({lanes + (which ? kDk : kDq) + part * HC + cb * 16}, ld);
         float(&a)[16] = ld[0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          a[i] = t < n ? a[i] : 0.f;
+        for (int j = 0; j < 2; ++j) {
+          const uint4 r = *reinterpret_cast<const uint4*>((which ? qs : ks) +
+                                                          piece<kQ>(t, (part * HC + cb * 16) / 8 + j));
+          const uint32_t* u = &r.x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int x = j * 8 + i * 2;
+            const float x0 = fmaf(own, lo_f(u[i]), a[x]), x1 = fmaf(own, hi_f(u[i]), a[x + 1]);
+            a[x] = t < n ? x0 : 0.f;
+            a[x + 1] = t < n ? x1 : 0.f;
+          }
         }
         const int col = part * HC + cb * 16;
         if (!there) continue;

@@ -325,8 +325,8 @@ e2ttt_status e2ttt_short_conv_step(const e2ttt_conv_shape* shape, const void* x,
  *   v, y [B, H, T, d_v], q, k [B, G, T, d_k] (act dtype); heads
  *   g*H/G .. (g+1)*H/G-1 share q and k of group g. (In state-space terms v is the
  *   input, k the input matrix and q the output matrix of the token.)
- *   dt [B, H, T] fp32 VALUES (after any softplus), A [H] fp32 (negative for a
- *   decaying state), D [H] fp32 or NULL (no skip), S [B, H, d_v, d_k] fp32.
+ *   dt [B, H, T] fp32 VALUES >= 0 (after any softplus), A [H] fp32 (negative for
+ *   a decaying state), D [H] fp32 or NULL (no skip), S [B, H, d_v, d_k] fp32.
  * States, decays and sums are held in fp32, the logarithms' sums in 64 bits. A
  * NaN or infinity in a valid token may reach every token of its chunk (at most
  * 128 tokens), earlier ones too, and all later ones.

@@ -374,7 +374,7 @@ def ssm_scan_fwd(q, k, v, dt, A, D=None, S0=None, lengths=None, *, save_states=F
                  stream=None):
     """Selective state-space scan S_t = exp(dt_t A) S_{t-1} + dt_t v_t k_t^T,
     y_t = S_t q_t + D v_t: v [B, H, T, d_v], q and k [B, G, T, d_k] (bf16 or
-    fp32; H / G heads share a group), dt [B, H, T], A and D [H], S0
+    fp32; H / G heads share a group), dt [B, H, T] >= 0, A and D [H], S0
     [B, H, d_v, d_k] fp32, lengths int32 [B] (a padded batch). Returns (y, S_end,
     saved), saved (what ssm_scan_bwd needs) None unless save_states."""
     dev, (shape, need, _, n_saved), state = _ssm_check(q, k, v, dt, A, D, lengths)

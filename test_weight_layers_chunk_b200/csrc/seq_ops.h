@@ -88,8 +88,7 @@ struct SsmBwdScratch {
   float *ends, *decay, *logs;  // [NC][B*H][P][N], [NC][B*H], the chunks' logarithms (tensor cores)
   float *dq, *dk;              // [B*G][parts][T][N] sums over part of a group's heads
   float* ddt;                  // [NPT][B*H][T]; the output itself where NPT is 1
-  double* dA;                  // [NC][NPT][B*H]; the parts cancel
-  float* dD;                   // [NC][NPT][B*H]
+  double *dA, *dD;             // [NC][NPT][B*H]; the parts cancel
 };
 size_t ssm_bwd_workspace_bytes(const SsmDims& s);
 cudaError_t ssm_bwd(const SsmBwdArgs& a);

@@ -315,15 +315,15 @@ __global__ void __launch_bounds__(kT)
                       const int* __restrict__ lengths, const float* __restrict__ states,
                       const float* __restrict__ ends, const T* __restrict__ dy,
                       float* __restrict__ dqp, float* __restrict__ dkp, T* __restrict__ dv,
-                      float* __restrict__ ddtp, double* __restrict__ dAp, float* __restrict__ dDp) {
+                      float* __restrict__ ddtp, double* __restrict__ dAp, double* __restrict__ dDp) {
   extern __shared__ float sm[];
   const Where w = where(s, lengths);
   const int Q = s.Q, N = s.N, XP = kXP, NP = pad8(N) + 4, QP = Q + 4;
   const ChunkLogs L(sm, Q);
-  // [4][Q]: row sums of Z off its diagonal, column sums of Z / eta off it, and the
-  // diagonals of Z / eta and of K
+  // [3][Q]: row sums of Z off its diagonal, column sums of Z / eta off it, and the
+  // diagonal of Z / eta
   float* dots = sm + kLogRows * Q;
-  float* scratch = dots + 4 * Q;
+  float* scratch = dots + 3 * Q;  // doubles too: Q is even
   float* qs = scratch + 16;
   float* ks = qs + Q * NP;
   float* Ss = ks + Q * NP;
@@ -364,10 +364,7 @@ __global__ void __launch_bounds__(kT)
         if (u < Q) {
           Ws[t * QP + u] = a;
           Ks[t * QP + u] = u <= t ? d * eta * kk.v[j][e] : 0.f;
-          if (u == t) {
-            dots[3 * Q + t] = kk.v[j][e];
-            dots[2 * Q + t] = r;
-          }
+          if (u == t) dots[2 * Q + t] = r;
         }
         m.v[j][e] = u < t && u < Q ? r : 0.f;  // Z / eta off the diagonal
         rows[e >> 1] = fmaf(m.v[j][e], eta, rows[e >> 1]);
@@ -477,12 +474,25 @@ __global__ void __launch_bounds__(kT)
     ip = fmaf(Ss[p * NP + n], Xs[p * NP + n], ip);
   }
   ip = block_sum0(ip, scratch);
+  // dD = sum dy v: fp64, as over a row it may cancel to almost nothing
+  double dsum = 0.0;
+  for (int i = threadIdx.x; i < Q * kSsmPT; i += kT) {
+    const int t = i / kSsmPT, p = i - t * kSsmPT;
+    dsum += (double)gs[t * XP + p] * xs[t * XP + p];
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) dsum += __shfl_xor_sync(~0u, dsum, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) reinterpret_cast<double*>(scratch)[threadIdx.x >> 5] = dsum;
+  __syncthreads();
   if (threadIdx.x < 32) {
     // ddt, dA, dD: lane l has the tokens l * K .. l * K + K - 1
     constexpr int K = R / 2;  // Q / 32
     const int lane = threadIdx.x;
     double in4[K], out4[K];
-    float a4[K], b4[K], src[K], as = 0.f, bs = 0.f, dD = 0.f;
+    float a4[K], b4[K], src[K], as = 0.f, bs = 0.f;
+    double dD = 0.0;
+    for (int i = 0; i < kT / 32; ++i) dD += reinterpret_cast<const double*>(scratch)[i];
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int r = lane * K + i;
@@ -498,7 +508,6 @@ __global__ void __launch_bounds__(kT)
       b4[i] = (float)out4[i];
       as += a4[i];
       bs += b4[i];
-      dD += dots[3 * Q + r];
     }
     float after = as, before = bs;  // of this lane's tokens on; up to them
 #pragma unroll
@@ -529,8 +538,6 @@ __global__ void __launch_bounds__(kT)
       const float x = fmaf(Ah, dl[i], dots[Q + r] + dots[2 * Q + r] + src[i]);
       if (w.t0 + r < s.T) out[r] = r < w.n ? x : 0.f;
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) dD += __shfl_xor_sync(~0u, dD, d);
     if (lane == 0) {
       const long long o = ((long long)w.c * s.NPT + w.pt) * s.B * s.H + w.bh;
       dAp[o] = dA;
@@ -570,7 +577,7 @@ __device__ __forceinline__ void group_sum(const float* part, int parts, long lon
   }
 }
 // dA[h], dD[h]: sums of part [rows][H], one block per head, in a fixed order.
-__device__ void head_sum(const double* dAp, const float* dDp, int rows, int H, int h, float* dA, float* dD) {
+__device__ void head_sum(const double* dAp, const double* dDp, int rows, int H, int h, float* dA, float* dD) {
   __shared__ double s[2][kT / 32];
   double a[2] = {0.0, 0.0};
   for (int i = threadIdx.x; i < rows; i += kT) {
@@ -597,7 +604,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kT)
     grad_sums_kernel(const float* __restrict__ dqp, const float* __restrict__ dkp, int parts,
                      long long row, T* __restrict__ dq, T* __restrict__ dk,
-                     const double* __restrict__ dAp, const float* __restrict__ dDp, int rows, int H,
+                     const double* __restrict__ dAp, const double* __restrict__ dDp, int rows, int H,
                      float* __restrict__ dA, float* __restrict__ dD, int z0) {
   griddep_wait();
   const int z = blockIdx.z + z0;
@@ -712,7 +719,7 @@ size_t out_smem(const SsmDims& s) {
                           (size_t)s.Q * kXP + (size_t)s.Q * (s.Q + 4));
 }
 size_t grad_smem(const SsmDims& s) {
-  return sizeof(float) * ((kLogRows + 4) * s.Q + 16 + (size_t)2 * (s.Q + kSsmPT) * (pad8(s.N) + 4) +
+  return sizeof(float) * ((kLogRows + 3) * s.Q + 16 + (size_t)2 * (s.Q + kSsmPT) * (pad8(s.N) + 4) +
                           (size_t)2 * s.Q * kXP + (size_t)2 * s.Q * (s.Q + 4) +
                           (size_t)12 * s.Q);
 }
@@ -745,7 +752,7 @@ size_t cut_bwd(const SsmDims& s, char* ws, float* ddt, SsmBwdScratch* w) {
   w->dk = take(sums);
   w->ddt = s.NPT > 1 ? take(s.NPT * BH * s.T * f) : ddt;
   w->dA = (double*)take((size_t)s.NC * s.NPT * BH * sizeof(double));
-  w->dD = take((size_t)s.NC * s.NPT * BH * f);
+  w->dD = (double*)take((size_t)s.NC * s.NPT * BH * sizeof(double));
   return o;
 }
 
@@ -823,7 +830,7 @@ static cudaError_t grad_sums_t(const SsmBwdArgs& a, const SsmBwdScratch& w, int 
   E2TTT_TRACE("ssm_grad_sums", a.st);
   return launch_pdl(vec ? grad_sums_kernel<T, 4> : grad_sums_kernel<T, 1>, grid, dim3(kT), 0, a.st,
                     (const float*)w.dq, (const float*)w.dk, parts, row, (T*)a.dq, (T*)a.dk, (const double*)w.dA,
-                    (const float*)w.dD, s.NC * s.NPT * s.B, s.H, a.dA, a.dD, direct ? 2 : 0);
+                    (const double*)w.dD, s.NC * s.NPT * s.B, s.H, a.dA, a.dD, direct ? 2 : 0);
 }
 cudaError_t ssm_grad_sums(const SsmBwdArgs& a, const SsmBwdScratch& w, int parts) {
   const SsmDims& s = a.s;

@@ -238,6 +238,7 @@ __device__ __forceinline__ uint32_t block_begin(uint64_t* bar, uint32_t* slot) {
 }
 template <int COLS>
 __device__ __forceinline__ void block_end(uint32_t tmem) {
+  cp_wait();  // (left over only where a wait gave up)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -737,8 +738,7 @@ struct GradOut {
   bf16 *dq16, *dk16; // the results themselves, where there is one part
   bf16* dv;
   float* ddt;
-  double* dA;
-  float* dD;
+  double *dA, *dD;
 };
 
 // All gradients of one chunk for a run of heads of one group (and their tiles of
@@ -753,7 +753,7 @@ struct GradOut {
 //   three terms, later overwritten by the two score matrices (X's first term stays)
 // What the next item reads comes in under this one: its S and X to registers once
 // the last products are issued, its v and dy once the scores are made.
-// 207 us for 128 heads x 2048 tokens (64 x 128 states), some 20000 cycles an item, of
+// 214 us for 128 heads x 2048 tokens (64 x 128 states), some 20000 cycles an item, of
 // which the MMAs are 4100: one chain of steps, since a second stream's tiles do not
 // fit. v, dy and dv by TMA took 218 us (more registers spilled), 256 threads with dq
 // and dk in registers 268.
@@ -768,8 +768,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTerm = NB * kPT * 128;  // bytes of one term of a state
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[kLogs];
-  __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[3][kQ], owned[kQ],
+  __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[2][kQ], owned[kQ],
       warp_ip[kThreads / 32];
+  __shared__ double warp_d[kThreads / 32];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
   uint8_t* qs = align1k(raw);
@@ -863,6 +864,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, St + 3 * kTerm, kPT / 16, true);
       mma<kQ, false, kPT, true, NB * 64>(tmem + 128, vs, Xs, kPT / 16, true);
       tc::mma_commit(&bar);
+    }
+    {
+      // dD = sum dy v: products of bf16 are exact in fp32; over a row the sum may
+      // cancel to almost nothing, so beyond a thread's 16 it is in fp64
+      float x = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t at = piece<kQ>(t, part * 2 + j);
+        const uint4 rv = *reinterpret_cast<const uint4*>(vs + at), rg = *reinterpret_cast<const uint4*>(gs + at);
+        const uint32_t *uv = &rv.x, *ug = &rg.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x = fmaf(lo_f(uv[i]), lo_f(ug[i]), fmaf(hi_f(uv[i]), hi_f(ug[i]), x));
+      }
+      double sum = x;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      if (lane == 0) warp_d[warp] = sum;
     }
     if (!(ok = done.wait())) break;
     // the states' parts of dq and dk, and their dots with q and k
@@ -993,9 +1011,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     rows[part][t] = zrow;
     if (part == quad) {  // the quarter that holds this row's diagonal block
       diag[0][t] = dr;
-      diag[1][t] = dd;
       owned[t] = fmaf(dd, L.eta[t], owned[t]);
-      if (it == i0) diag[2][t] = dm;
+      if (it == i0) diag[1][t] = dm;
     }
     publish();
     if (threadIdx.x == 0) {
@@ -1061,14 +1078,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t0 + r < s.T) out[r] = r < n ? x : 0.f;
         }
       } else {
-        double in[4], out[4];
-        float dsum = 0.f;
+        double in[4], out[4], dsum = lane < kThreads / 32 ? warp_d[lane] : 0.0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = lane * 4 + i;
           in[i] = in4[i];
           out[i] = (double)L.eta[r] * src4[i];
-          dsum += diag[1][r];
         }
         const double dA = decay_gradient<4>([&](int cb, int i) { return rows[cb][lane * 4 + i]; },
                                             [&](int qd, int i) { return cols[qd][lane * 4 + i]; }, in, out,
@@ -1088,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ld[2][16];
       tmem_ld16<2>({lanes + part * 16, lanes + 64 + part * 16}, ld);
       float(&a1)[16] = ld[0], (&a2)[16] = ld[1];
-      const float e = L.end[t], eta = L.eta[t], Dh = fmaf(eta, diag[2][t], D ? D[h] : 0.f);
+      const float e = L.end[t], eta = L.eta[t], Dh = fmaf(eta, diag[1][t], D ? D[h] : 0.f);
       bf16* out = o.dv + vo + (long long)t * s.P + part * 16;
       if (t0 + t < s.T)
 #pragma unroll

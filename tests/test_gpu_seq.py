@@ -287,6 +287,22 @@ def test_scan_no_decay_and_growth(E, act):
     scan_check(act, x, None, y, S, grads)
 
 
+@pytest.mark.parametrize("act,T,P,N", [("f32", 500, 64, 64), ("f32", 100, 40, 200), ("bf16", 500, 64, 128),
+                                       ("bf16", 77, 48, 40), ("bf16", 200, 33, 17)])
+def test_scan_skip_gradient_of_one_head(E, act, T, P, N):
+    """dD = sum dy v of one row, whose terms cancel: products and sums are fp64 (fp32
+    over at most 16 exact products of bf16, 16 roundings), then dD is rounded once."""
+    x = scan_inputs(act, 1, 1, 1, T, P, N, True, False, False, seed=T + P)
+    x["dy"][:, :, 1::2] = -x["dy"][:, :, :-1:2]
+    x["v"][:, :, 1::2] = x["v"][:, :, :-1:2].clone()  # pairs cancel; what is left
+    x["dy"][0, 0, 3, 5] += 0.5                               # is one element's change
+    g, _ = to_gpu(x, None, T)
+    terms = host(x["dy"]) * host(x["v"])
+    bound = T * P * 2.0 ** -53 + (16 * U32 if act == "bf16" else 0.0)
+    got = run_scan(E, g, None)[2]["dD"]
+    close("dD", got, terms.sum()[None], bound * np.abs(terms).sum() + U32 * np.abs(terms.sum()) + 1e-30)
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 def test_scan_zero_steps(E, act):
     """dt = 0: the token leaves the state as it is, and its gradients are those of that."""

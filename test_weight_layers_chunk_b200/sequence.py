@@ -213,7 +213,8 @@ def _guard(dev, stream):
             yield
         else:
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
+                # (0, the default stream's handle, would be a new stream to ExternalStream)
+                stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
             elif stream.device.index != dev:
                 _refuse(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
             with torch.cuda.stream(stream):

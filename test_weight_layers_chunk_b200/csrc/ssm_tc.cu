@@ -971,14 +971,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             kk[i] = u <= t ? kk[i] : 0.f;
           }
         }
+        // q_t.k_t, the same for every item (before the decay, whose NaN would be one head's)
+        if (part == quad && it == i0)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dm = u0 + i == t ? m[i] : dm;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           m[i] *= e[i];
           off[i] = m[i] * kk[i];
         }
-        if (part == quad && it == i0)  // q_t.k_t, the same for every item
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dm = u0 + i == t ? m[i] : dm;
         if (part == quad)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {

@@ -39,3 +39,45 @@ def test_stream_handle_of_the_default_stream(E, monkeypatch):
             E.short_conv_fwd(x, w, stream=side.cuda_stream)
     torch.cuda.synchronize()
     assert used == ([0] * 4 + [side.cuda_stream] * 2) * 2
+
+
+SPREAD = [  # act, B, H, G, T, P, N: one chunk and several, several heads a block, both tile widths, and fp32
+    ("bf16", 1, 3, 3, 1, 64, 64), ("bf16", 74, 6, 2, 40, 64, 64), ("bf16", 74, 6, 2, 140, 40, 128),
+    ("bf16", 1, 3, 1, 300, 24, 200), ("f32", 2, 3, 1, 140, 24, 20),
+]
+
+
+def with_nan(E, case, what):
+    """What the scan and its gradients give without and with a NaN in head 0's decay,
+    step, state or input, the token that it is in, and the inputs."""
+    act, B, H, G, T, P, N = case
+    x = scan_inputs(act, B, H, G, T, P, N, True, True, True, seed=T + N)
+    g = {n: t.cuda() for n, t in x.items()}
+
+    def run():
+        y, S, saved = E.ssm_scan_fwd(g["q"], g["k"], g["v"], g["dt"], g["A"], g["D"], g["S0"], save_states=True)
+        return dict(E.ssm_scan_bwd(g["q"], g["k"], g["v"], g["dt"], g["A"], saved, g["dy"], g["D"], g["dS_end"]),
+                    y=y, S_end=S)
+
+    clean, at = run(), T // 2
+    nan = float("nan")
+    if what == "A":
+        g["A"][0], at = nan, 0
+    elif what == "dt":
+        g["dt"][:, 0, at] = nan
+    elif what == "S0":
+        g["S0"][:, 0], at = nan, 0
+    else:
+        g["v"][:, 0, at] = nan
+    return clean, run(), at, g
+
+
+@pytest.mark.parametrize("what", ["A", "dt", "S0", "v"])
+@pytest.mark.parametrize("case", SPREAD, ids=[f"{c[0]}-{'x'.join(map(str, c[1:]))}" for c in SPREAD])
+def test_nan_stays_with_its_head(E, case, what):
+    """The other heads' results are those without it, bit for bit."""
+    clean, got, _, _ = with_nan(E, case, what)
+    for n in ("y", "S_end", "dv", "ddt", "dS0"):
+        assert torch.equal(got[n][:, 1:], clean[n][:, 1:]), n
+    for n in ("dA", "dD"):
+        assert torch.equal(got[n][1:], clean[n][1:]), n

@@ -33,7 +33,7 @@ __device__ __forceinline__ float ex2(float x) {
 // the nearest whole number and |f| <= 1/2, by the exponential series to the eighth
 // power (what is left out is below 2e-10).
 __device__ __forceinline__ float exp2_rounded(double x) {
-  x = fmin(fmax(x, -200.0), 200.0);  // 2^x is zero or infinite beyond
+  x = x < -200.0 ? -200.0 : x > 200.0 ? 200.0 : x;  // 2^x is zero or infinite beyond; a NaN stays one
   const double n = rint(x);
   const float f = (float)(x - n) * 0.69314718055994531f;
   float p = 1.0f / 40320.0f;

@@ -81,3 +81,19 @@ def test_nan_stays_with_its_head(E, case, what):
         assert torch.equal(got[n][:, 1:], clean[n][:, 1:]), n
     for n in ("dA", "dD"):
         assert torch.equal(got[n][1:], clean[n][1:]), n
+
+
+@pytest.mark.parametrize("what", ["A", "dt", "S0", "v"])
+@pytest.mark.parametrize("case", SPREAD, ids=[f"{c[0]}-{'x'.join(map(str, c[1:]))}" for c in SPREAD])
+def test_nan_reaches_what_follows(E, case, what):
+    """Its own head's state is lost from there on; it does not count as no state at all."""
+    _, got, at, g = with_nan(E, case, what)
+    assert got["S_end"][:, 0].isnan().all()
+    assert got["y"][:, 0, at:].isnan().all()
+    if what in ("A", "dt"):  # the gradients pass every decay on the way to the row's start
+        assert got["dS0"][:, 0].isnan().all() and got["ddt"][:, 0, :at + 1].isnan().all() and got["dA"][0].isnan()
+    if what == "A":  # and a single token does the same
+        state = g["S0"].clone()
+        state[state.isnan()] = 0.0
+        E.ssm_step(*(g[n][:, :, 0].contiguous() for n in ("q", "k", "v", "dt")), state, g["A"])
+        assert state[:, 0].isnan().all() and not state[:, 1:].isnan().any()

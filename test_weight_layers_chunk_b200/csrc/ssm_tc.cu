@@ -152,9 +152,12 @@ __device__ __forceinline__ void load8f(float (&f)[8], const float* p, int left) 
   }
 }
 
-// f as three bf16 terms, its mantissa's first, second and third eight bits: each is
-// what the ones before leave, cut off, so that the three add up to f exactly (above
-// the smallest exponents) and a term is the upper half of a word as it stands.
+// f as three bf16 terms that add up to it exactly (above the smallest exponents): each
+// is what the ones before leave, cut off to its first eight bits, so that it is the
+// upper half of a word as it stands. ROUND: the first term is f rounded to bf16, for a
+// product that takes it alone (cut off, it would lean towards zero by 2^-9 on average);
+// what that leaves has at most 16 bits for the other two.
+template <bool ROUND = false>
 __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
   uint32_t* o[3] = {&t[0].x, &t[1].x, &t[2].x};
 #pragma unroll
@@ -162,10 +165,10 @@ __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
     float a = f[2 * i], b = f[2 * i + 1];
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-      o[j][i] = __byte_perm(ua, ub, 0x7632);
-      a -= __uint_as_float(ua & 0xffff0000u);
-      b -= __uint_as_float(ub & 0xffff0000u);
+      const uint32_t w = ROUND && j == 0 ? pack2(a, b) : __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+      o[j][i] = w;
+      a -= lo_f(w);
+      b -= hi_f(w);
     }
   }
 }
@@ -845,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         split3(Sf[i], term);
 #pragma unroll
         for (int m = 0; m < 3; ++m) *reinterpret_cast<uint4*>(St + m * kTerm + at) = term[m];
-        split3(Xf[i], term);
+        split3<true>(Xf[i], term);  // dv takes the first one alone
         *reinterpret_cast<uint4*>(Xs + at) = term[0];
         *reinterpret_cast<uint4*>(St + 3 * kTerm + at) = term[1];
         *reinterpret_cast<uint4*>((NB == 1 ? St + 4 * kTerm : Xs + kTerm) + at) = term[2];

@@ -132,3 +132,33 @@ def test_state_gradient_does_not_lean(E, N):
     dv = E.ssm_scan_bwd(g["q"], g["k"], g["v"], g["dt"], g["A"], saved, g["dy"], dS_end=g["dS_end"])["dv"].double()
     want = g["dt"].double()[..., None] * (g["k"].double() @ g["dS_end"].double().transpose(-1, -2))
     assert abs(float(((dv - want) * want).sum() / want.square().sum())) <= 6 * 2 * 0.43 * UBF * 2.0 ** -7.5
+
+
+@pytest.mark.parametrize("N", [16, 18, 128])
+@pytest.mark.parametrize("log", [1e-3, 1e-4])
+def test_long_generation_keeps_the_decay(E, log, N):
+    """n single tokens that add nothing: S = S0 e^{n dt A}. Each of the n states is
+    rounded once, by 2^-24 and either sign: sqrt(n) 2^-24, held to six times that. A
+    decay that is itself off by half a unit, 2^-25, would be off n times the same way."""
+    B, H, P, n = 1, 32, 4, 4000
+    r = torch.Generator().manual_seed(N)
+    A = -(0.5 + torch.rand(H, generator=r)).cuda()
+    dt = torch.full((B, H), log, device="cuda")
+    S0 = torch.randn(B, H, P, N, generator=r).cuda()
+    S, v, k = S0.clone(), torch.zeros(B, H, P, device="cuda"), torch.ones(B, 1, N, device="cuda")
+    for _ in range(n):
+        E.ssm_step(k, k, v, dt, S, A)
+    want = S0.double() * torch.exp(n * dt.double() * A.double())[..., None, None]
+    off = ((S.double() - want) / want).abs()
+    assert float(off.max()) <= 6 * n ** 0.5 * U32, float(off.max())
+
+
+def test_steps_of_an_infinite_state(E):
+    """An infinite state stays infinite under a decay, and under none (dt = 0)."""
+    for dt in (0.0, 0.1, 2.0):
+        S = torch.full((1, 1, 2, 8), float("inf"), device="cuda")
+        S[:, :, 1] = 1.0
+        one = torch.ones(1, 1, 8, device="cuda")
+        E.ssm_step(one, one, torch.ones(1, 1, 2, device="cuda"), torch.full((1, 1), dt, device="cuda"), S,
+                   torch.tensor([-1.0], device="cuda"))
+        assert S[0, 0, 0].isinf().all() and S[0, 0, 1].isfinite().all()

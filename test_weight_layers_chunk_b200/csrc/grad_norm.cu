@@ -69,6 +69,12 @@ __device__ __forceinline__ float squares(const uint4& raw) {
   return s;
 }
 __device__ __forceinline__ bool fits(float s) { return s > 1e-24f && s < 1e37f; }
+// Zeros of either sign throughout, whose sum is exact: whole rows of a gradient are zero
+// where a token or an expert was not used.
+template <typename T>
+__device__ __forceinline__ bool zeros(const uint4& raw) {
+  return ((raw.x | raw.y | raw.z | raw.w) & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) == 0;
+}
 template <typename T>
 __device__ __forceinline__ double square1(T v) {
   const double x = to_f<T>(v);
@@ -97,7 +103,7 @@ __device__ double piece_squares(const Item& it, unsigned piece) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       q[u] = squares<T>(r[u]);
-      all = all && (fits(q[u]) || i + u * kThreads >= nv);
+      all = all && (fits(q[u]) || zeros<T>(r[u]));  // (those past the end are zeros)
     }
     if (all) {
 #pragma unroll

@@ -54,12 +54,21 @@ _ACT = {torch.bfloat16: BF16, torch.float32: F32}
 
 
 # ---------------------------------------------------------------- C entry points
+def _filled(kind, sizes):
+    """A shape struct, whose fields are C ints: what does not fit one is refused (ctypes
+    would keep the lower 32 bits)."""
+    for (name, _), n in zip(kind._fields_, sizes):
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise E2TTTError(ERR_INVALID_ARG, f"{name}={n} does not fit a shape")
+    return kind(*sizes)
+
+
 def make_conv_shape(B, H, T, d, W, act=BF16, silu=True) -> e2ttt_conv_shape:
-    return e2ttt_conv_shape(B, H, T, d, W, act, int(silu))
+    return _filled(e2ttt_conv_shape, (B, H, T, d, W, act, int(silu)))
 
 
 def make_ssm_shape(B, H, G, T, d_k, d_v, act=BF16) -> e2ttt_ssm_shape:
-    return e2ttt_ssm_shape(B, H, G, T, d_k, d_v, act)
+    return _filled(e2ttt_ssm_shape, (B, H, G, T, d_k, d_v, act))
 
 
 def _nbytes(workspace):
@@ -254,13 +263,13 @@ def _scratch(ws, need, like):
 # Shapes and the sizes that follow from them, by value.
 @functools.lru_cache(maxsize=1024)
 def _conv_shape(*sizes):
-    shape = e2ttt_conv_shape(*sizes)
+    shape = _filled(e2ttt_conv_shape, sizes)
     return ctypes.byref(shape), e2ttt_short_conv_workspace_bytes(shape)
 
 
 @functools.lru_cache(maxsize=1024)
 def _ssm_shape(*sizes):
-    shape = e2ttt_ssm_shape(*sizes)
+    shape = _filled(e2ttt_ssm_shape, sizes)
     return (ctypes.byref(shape), e2ttt_ssm_workspace_bytes(shape, 0), e2ttt_ssm_workspace_bytes(shape, 1),
             e2ttt_ssm_saved_bytes(shape))
 

@@ -409,6 +409,14 @@ e2ttt_status e2ttt_workspace_status(const void* workspace, void* stream);
  * normally. The hook disarms itself once used; on = 0 disarms it. */
 void e2ttt_test_stall_next_forward(int on);
 
+/* A test hook for the tensor-core kernels of the state-space scan: one block takes a
+ * wait for run out, in the next launch that has wait number `wait`: 1 the chunk states'
+ * products (forward, or the gradients' adjoint), 2 the scores, 3 an item's loads, 4 an
+ * item's outputs (forward), 5, 6 and 7 the gradients' three steps; up to 4 it is a single
+ * thread of the block. The block gives up as above; all other waits are as always.
+ * Disarms itself once used; 0 disarms it. */
+void e2ttt_test_stall_next_scan(int wait);
+
 /* Launch tracing. While enabled, every kernel the library launches is
  * bracketed by a pair of CUDA events recorded on its launch stream (events are
  * created by the library and reused; no device memory is allocated).

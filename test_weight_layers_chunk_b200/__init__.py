@@ -298,6 +298,7 @@ _SEQUENCE = ("make_conv_shape", "make_ssm_shape", "short_conv_fwd", "short_conv_
              "e2ttt_short_conv_workspace_bytes", "e2ttt_short_conv_fwd", "e2ttt_short_conv_bwd",
              "e2ttt_short_conv_step", "e2ttt_ssm_workspace_bytes", "e2ttt_ssm_saved_bytes",
              "e2ttt_ssm_scan_fwd", "e2ttt_ssm_scan_bwd", "e2ttt_ssm_step",
+             "e2ttt_test_stall_next_scan",
              "e2ttt_grad_workspace_bytes", "e2ttt_grad_norm", "e2ttt_clip_grad_norm")
 
 

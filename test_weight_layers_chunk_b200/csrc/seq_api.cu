@@ -366,6 +366,8 @@ e2ttt_status e2ttt_ssm_step(const e2ttt_ssm_shape* s, const void* q, const void*
   })
 }
 
+void e2ttt_test_stall_next_scan(int wait) { arm_scan_stall(wait); }
+
 size_t e2ttt_grad_workspace_bytes(int count) { return count < 0 ? 0 : grad_workspace_bytes(count); }
 
 e2ttt_status e2ttt_grad_norm(const void* const* g, const size_t* n, const int* act, int count,

@@ -63,6 +63,8 @@ struct SsmFwdArgs {
 cudaError_t ssm_fwd(const SsmFwdArgs& a);     // CUDA cores, any shape
 cudaError_t ssm_tc_fwd(const SsmFwdArgs& a);  // tensor cores, shapes with tc set
 size_t ssm_tc_logs_bytes(const SsmDims& s);
+// Test hook behind e2ttt_test_stall_next_scan.
+void arm_scan_stall(int wait);
 // The states' passage along the chunks (back: their adjoint's, from the end),
 // from `first` (NULL: zero); what is left after the last chunk goes to `last`, a
 // bf16 copy of the states to `copy` (may be NULL); without `keep` only that.

@@ -12,6 +12,7 @@
 // decayed scores, the state in y and dv); where the product ends in an fp32
 // result (the states, and the dots behind ddt and dA) it enters as three bf16
 // terms that together hold all 24 bits of it, each with a product of its own.
+#include <atomic>
 #include <initializer_list>
 
 #include "ssm.cuh"
@@ -60,19 +61,28 @@ __device__ __forceinline__ void mma(uint32_t acc, const uint8_t* a, const uint8_
     tc::mma_bf16(acc, da + step_off<AROWS, AMN>(k), db + step_off<BROWS, BMN>(k), id, add || k);
 }
 
+// The waits that the failure-detection test hook (e2ttt_test_stall_next_scan) can make
+// block (0, 0, 0) of the next launch that has them take for run out.
+enum Stall : int { kNone, kStates, kScores, kRows, kOutputs, kDots, kPairs, kResults };
+__device__ __forceinline__ bool stalled(int stall, int at) {
+  return stall == at && blockIdx.x + blockIdx.y + blockIdx.z == 0;
+}
+
 // The waits of one block on its MMAs: one mbarrier, one phase per commit.
 struct Mmas {
   uint64_t* bar;
   uint32_t phase;
   int* status;
   // True (for the whole block) once the last commit has completed; false, with
-  // the status word set, after about a second without it.
-  __device__ __forceinline__ bool wait() {
-    const bool ok = tc::mbar_wait(bar, phase);
-    if (!ok && threadIdx.x == 0) atomicExch(status, tc2::kErrMma);
+  // the status word set, where a thread waited about a second without it.
+  __device__ __forceinline__ bool wait(bool stall) {
+    const bool ok = tc::mbar_wait(bar, phase) && !stall;
     const bool all = __syncthreads_and(ok);
-    // on giving up: once more, so that the MMAs do not outlive their memory
-    if (!all) (void)tc::mbar_wait(bar, phase);
+    if (!all) {  // whichever thread it was
+      if (threadIdx.x == 0) atomicExch(status, tc2::kErrMma);
+      // once more, so that the MMAs do not outlive their memory
+      (void)tc::mbar_wait(bar, phase);
+    }
     phase ^= 1u;
     tc::tc_fence_after();
     return all;
@@ -330,8 +340,8 @@ struct GroupMmas {
   uint32_t phase;
   int* status;
   int wg;
-  __device__ __forceinline__ bool wait(bool so_far = true) {
-    const bool ok = tc::mbar_wait(bar, phase) && so_far;
+  __device__ __forceinline__ bool wait(bool stall, bool so_far = true) {
+    const bool ok = tc::mbar_wait(bar, phase) && so_far && !(stall && threadIdx.x == kHalf - 1);
     if (!ok) atomicExch(status, tc2::kErrMma);
     const bool all = group_and(wg, ok);
     if (!all) (void)tc::mbar_wait(bar, phase);
@@ -394,7 +404,7 @@ template <int REV, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     state_kernel(SsmDims s, const bf16* __restrict__ x, const bf16* __restrict__ y,
                  const float* __restrict__ logs, const int* __restrict__ lengths,
-                 float* __restrict__ states, int per, int* __restrict__ status) {
+                 float* __restrict__ states, int per, int* __restrict__ status, int stall) {
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bar, gbar[2];
   __shared__ uint32_t slot;
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mma_commit(&gbar[wg]);
     }
     if (it + 2 < m.i1) fetch(it + 2);
-    if (!done.wait()) break;
+    if (!done.wait(stalled(stall, kStates))) break;
     const int h = m.head(it), p0 = m.first_row(it), bh = m.b * s.H + h;
     const int np = min(kPT, s.P - p0);
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -496,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const bf16* __restrict__ v, const float* __restrict__ logs,
                const float* __restrict__ D, const int* __restrict__ lengths,
                const bf16* __restrict__ states, bf16* __restrict__ y, int per,
-               int* __restrict__ status, const __grid_constant__ OutMaps maps) {
+               int* __restrict__ status, int stall, const __grid_constant__ OutMaps maps) {
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[2][kLogs], own[kQ];
   __shared__ uint64_t bar, gbar[2], sbar[2], full[2];
@@ -572,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t kYi = 128 + wg * 128, kYd = kYi + 64;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-  if (first.wait()) {
+  if (first.wait(stalled(stall, kScores) && threadIdx.x == kThreads - 1)) {
     // q_t.k_t; the scores above the diagonal blocks are zero for every item
     if (wg == 0 && half == 0) {
       float a[32], x = 0.f;
@@ -605,11 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_wait();
       group_publish(wg);  // the item's logs, and what the threads loaded, are there
       if (leader) {
-        lead_ok = !tma || tc::mbar_wait(&full[wg], phase);
+        lead_ok = !tma || (tc::mbar_wait(&full[wg], phase) && !stalled(stall, kRows));
         mma<kQ, false, kPT, false, 64>(tmem + kYi, qs, Ss, nsteps, false);
         tc::mma_commit(&sbar[wg]);
       }
-      if (it + 2 < m.i1) {
+      const bool more = it + 2 < m.i1 && lead_ok;  // (on giving up no load is added to one that has not landed)
+      if (more) {
         fetch_logs(it + 2);
         if (tma && leader) tc::bulk_wait_read<0>();  // that buffer's y is on its way
         fetch_rows(it + 2, buf ^ 1);
@@ -659,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_commit(&gbar[wg]);
       }
       if (!tma || leader) lead_ok = tc::mbar_wait(&sbar[wg], phase) && lead_ok;  // the state's tile is free
-      if (it + 2 < m.i1) fetch_state(it + 2);
-      if (!done.wait(lead_ok)) {
+      if (more) fetch_state(it + 2);
+      if (!done.wait(stalled(stall, kOutputs), lead_ok)) {
         gave_up = true;
         break;
       }
@@ -767,12 +778,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float* __restrict__ logs, const float* __restrict__ A,
                 const float* __restrict__ D, const int* __restrict__ lengths,
                 const float* __restrict__ states, const float* __restrict__ ends, GradOut o,
-                int per, int* __restrict__ status) {
+                int per, int* __restrict__ status, int stall) {
   constexpr int kTerm = NB * kPT * 128;  // bytes of one term of a state
   extern __shared__ uint8_t raw[];
   __shared__ __align__(16) float slog[kLogs];
   __shared__ float rows[4][kQ], cols[4][kQ], rdr[4][kQ], src[4][kQ], diag[2][kQ], owned[kQ],
       warp_ip[kThreads / 32];
+  __shared__ int lost;  // the wait that the test hook makes this block lose
   __shared__ double warp_d[kThreads / 32];
   __shared__ uint64_t bar;
   __shared__ uint32_t slot;
@@ -787,6 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int c = blockIdx.x, bg = blockIdx.y, b = bg / s.G, g = bg - b * s.G, split = blockIdx.z;
   const int HG = s.H / s.G, items = HG * s.NPT, BH = s.B * s.H, t0 = c * kQ;
   const ChunkLogs L(slog, kQ);
+  if (threadIdx.x == 0) lost = stalled(stall, stall) ? stall : kNone;
   const uint32_t tmem = block_begin<512>(&bar, &slot);
   griddep_wait();
   griddep_launch_dependents();
@@ -885,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
       if (lane == 0) warp_d[warp] = sum;
     }
-    if (!(ok = done.wait())) break;
+    if (!(ok = done.wait(lost == kDots))) break;
     // the states' parts of dq and dk, and their dots with q and k
     {
       const float f = L.start[t], e = L.end[t], ee = e * L.eta[t];
@@ -929,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma<kQ, false, kQ, false, 128>(tmem + 128, gs, vs, kPT / 16, false);
       tc::mma_commit(&bar);
     }
-    if (!(ok = done.wait())) break;
+    if (!(ok = done.wait(lost == kPairs))) break;
     if (it + 1 < i1) fetch_rows(it + 1, (it - i0 + 1) & 1);  // v has done its part
     // the decayed scores, and the row and column sums of Z off its diagonal
     float zrow = 0.f, dr = 0.f, dd = 0.f, dm = 0.f;
@@ -1102,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-    if (!(ok = done.wait())) break;
+    if (!(ok = done.wait(lost == kResults))) break;
     {
       float ld[2][16];
       tmem_ld16<2>({lanes + part * 16, lanes + 64 + part * 16}, ld);
@@ -1254,6 +1267,13 @@ cudaError_t allow_smem(F* f, size_t bytes) {
   return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+// The wait that the test hook has armed, for a launch that has waits first .. last.
+std::atomic<int> g_stall{kNone};
+int take_stall(int first, int last) {
+  int armed = g_stall.load(std::memory_order_relaxed);
+  return armed >= first && armed <= last && g_stall.compare_exchange_strong(armed, kNone) ? armed : kNone;
+}
+
 bool vectors(const SsmDims& s, std::initializer_list<const void*> ps) {
   if (s.N % 8 || s.P % 8) return false;
   for (const void* p : ps)
@@ -1262,6 +1282,8 @@ bool vectors(const SsmDims& s, std::initializer_list<const void*> ps) {
 }
 
 }  // namespace
+
+void arm_scan_stall(int wait) { g_stall.store(wait >= kStates && wait <= kResults ? wait : kNone); }
 
 size_t ssm_tc_logs_bytes(const SsmDims& s) {
   return (size_t)s.B * s.H * s.NC * kLogs * sizeof(float);
@@ -1287,7 +1309,7 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
     if ((e = allow_smem(kern, state_smem())) != cudaSuccess) return e;
     const dim3 grid = item_grid(s, item_parts(s, 2, 1.5, 0), &per);
     e = launch_pdl(kern, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.dy, (const bf16*)a.q,
-                   (const float*)w.logs, a.lengths, w.ends, per, w.status);
+                   (const float*)w.logs, a.lengths, w.ends, per, w.status, take_stall(kStates, kStates));
     if (e != cudaSuccess) return e;
   }
   if ((e = ssm_carry(s, true, a.dS_end, w.decay, w.ends, a.dS0, nullptr, true, a.st)) != cudaSuccess) return e;
@@ -1301,7 +1323,7 @@ cudaError_t ssm_tc_bwd(const SsmBwdArgs& a, const SsmBwdScratch& w) {
     const dim3 grid = item_grid(s, parts, &per);
     e = launch_pdl(kern, grid, dim3(kThreads), smem, a.st, s, (const bf16*)a.q,
                    (const bf16*)a.k, (const bf16*)a.v, (const bf16*)a.dy, (const float*)w.logs, a.A, a.D, a.lengths,
-                   a.states, (const float*)w.ends, o, per, w.status);
+                   a.states, (const float*)w.ends, o, per, w.status, take_stall(kDots, kResults));
     if (e != cudaSuccess) return e;
   }
   return ssm_grad_sums(a, w, parts);
@@ -1325,7 +1347,7 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
     if ((e = allow_smem(kern, state_smem())) != cudaSuccess) return e;
     const dim3 grid = item_grid(s, item_parts(s, 2, 1.5, 0), &per);
     e = launch_pdl(kern, grid, dim3(kThreads), state_smem(), a.st, s, (const bf16*)a.v, (const bf16*)a.k,
-                   (const float*)a.logs, a.lengths, a.states, per, a.status);
+                   (const float*)a.logs, a.lengths, a.states, per, a.status, take_stall(kStates, kStates));
     if (e != cudaSuccess) return e;
   }
   if ((e = ssm_carry(s, false, a.S0, a.decay, a.states, a.S_end, a.starts, a.keep, a.st)) != cudaSuccess) return e;
@@ -1341,7 +1363,7 @@ cudaError_t ssm_tc_fwd(const SsmFwdArgs& a) {
     return cudaErrorNotSupported;
   return launch_pdl(kern, grid, dim3(kThreads), smem, a.st, s, (const bf16*)a.q, (const bf16*)a.k,
                     (const bf16*)a.v, (const float*)a.logs, a.D, a.lengths, (const bf16*)a.starts,
-                    (bf16*)a.y, per, a.status, maps);
+                    (bf16*)a.y, per, a.status, take_stall(kScores, kOutputs), maps);
 }
 
 }  // namespace e2ttt

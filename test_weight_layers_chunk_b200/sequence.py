@@ -42,6 +42,7 @@ for _name, (_res, _args) in {
     "e2ttt_ssm_scan_fwd": (_I, [_M] + [_P] * 12 + [_Z, _P]),
     "e2ttt_ssm_scan_bwd": (_I, [_M] + [_P] * 18 + [_Z, _P]),
     "e2ttt_ssm_step": (_I, [_M] + [_P] * 9),
+    "e2ttt_test_stall_next_scan": (None, [_I]),
     "e2ttt_grad_workspace_bytes": (_Z, [_I]),
     "e2ttt_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _Z, _P]),
     "e2ttt_clip_grad_norm": (_I, [_P, _P, _P, _P, _I, ctypes.c_float, _P, _P, _Z, _P]),
@@ -140,6 +141,11 @@ def e2ttt_ssm_step(shape, q, k, v, dt, A, D, S, y, stream=None, raw=False):
     return _done(_lib.e2ttt_ssm_step(
         ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(D), _ptr(S), _ptr(y),
         _stream(stream) if not raw else stream), raw)
+
+
+def e2ttt_test_stall_next_scan(wait: int) -> None:
+    """Failure-detection test hook: wait number `wait` of the next tensor-core scan times out."""
+    _lib.e2ttt_test_stall_next_scan(int(wait))
 
 
 def e2ttt_grad_workspace_bytes(count) -> int:

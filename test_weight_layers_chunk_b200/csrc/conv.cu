@@ -473,12 +473,13 @@ __global__ void __launch_bounds__(kThreads, W <= 4 ? 2 : 1)
 }
 
 // dw [H][d][W], dbias [H][d]: sums of `n` partial rows, in order. A block's 8
-// warps share the rows of 32 channels.
+// warps share the rows of 32 channels. Resets the workspace's status word: nothing waits.
 template <int W>
 __global__ void __launch_bounds__(256) conv_sum_kernel(const float* __restrict__ part, int n, int H,
                                                        int d, float* __restrict__ dw,
-                                                       float* __restrict__ dbias) {
+                                                       float* __restrict__ dbias, int* __restrict__ status) {
   __shared__ float s[8][32];
+  if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0) *status = 0;
   const int c = blockIdx.x * 32 + threadIdx.x % 32, way = threadIdx.x / 32;
   const int j = blockIdx.y, h = blockIdx.z;
   float a = 0.f;
@@ -593,6 +594,7 @@ cudaError_t bwd_t(const ConvArgs& a, const void* dy, const void* dstate_end, voi
   const int gx = bwd_blocks_x(a.s, g);
   dim3 grid(gx, a.s.B * a.s.H, (g.nvec + g.nvt - 1) / g.nvt);
   const int threads = g.nvt * g.rows;
+  float* part = (float*)((char*)ws + kStatusBytes);
   {
     E2TTT_TRACE("conv_bwd", a.st);
     auto kern = a.s.silu ? conv_bwd_kernel<T, W, VEC, true> : conv_bwd_kernel<T, W, VEC, false>;
@@ -601,13 +603,13 @@ cudaError_t bwd_t(const ConvArgs& a, const void* dy, const void* dstate_end, voi
     if (e != cudaSuccess) return e;
     kern<<<grid, threads, smem, a.st>>>(
         g, (const T*)a.x, a.w, a.bias, (const T*)a.state, a.lengths, (const T*)dy,
-        (const T*)dstate_end, (T*)dx, (T*)dstate, (float*)ws);
+        (const T*)dstate_end, (T*)dx, (T*)dstate, part);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   E2TTT_TRACE("conv_sum", a.st);
   conv_sum_kernel<W><<<dim3((a.s.d + 31) / 32, W + 1, a.s.H), 256, 0, a.st>>>(
-      (const float*)ws, a.s.B * gx, a.s.H, a.s.d, dw, dbias);
+      part, a.s.B * gx, a.s.H, a.s.d, dw, dbias, (int*)ws);
   return cudaGetLastError();
 }
 
@@ -651,7 +653,7 @@ size_t conv_bwd_workspace_bytes(const ConvDims& s) {
     const size_t n = (size_t)s.B * bwd_blocks_x(s, geometry(s, vec, true)) * s.H * (s.W + 1) * s.d * sizeof(float);
     if (n > most) most = n;
   }
-  return most;
+  return kStatusBytes + most;
 }
 
 cudaError_t conv_fwd(const ConvArgs& a, void* y, void* state_end) {

@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(kThreads, 4)
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* __restrict__ part, int n,
-                                                             float* __restrict__ norm) {
+                                                             float* __restrict__ norm, int* __restrict__ status) {
   const double s = partials_sum(part, n);
-  if (threadIdx.x == 0) *norm = (float)sqrt(s);
+  if (threadIdx.x == 0) *norm = (float)sqrt(s), *status = 0;
 }
 
 template <typename T>
@@ -192,9 +192,9 @@ __device__ void piece_scale(const Item& it, unsigned piece, float scale) {
 template <int MAX>
 __global__ void __launch_bounds__(kThreads, 4)
     grad_clip_kernel(const __grid_constant__ List<MAX> l, const double* __restrict__ part, int n,
-                     float max_norm, float* __restrict__ norm) {
+                     float max_norm, float* __restrict__ norm, int* __restrict__ status) {
   const float total = (float)sqrt(partials_sum(part, n));
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total, *status = 0;
   const float c = max_norm / (total + 1e-6f);
   const float scale = c > 1.f ? 1.f : c;  // a NaN norm scales by NaN
   const unsigned p0 = range_start(l.pieces, blockIdx.x), p1 = range_start(l.pieces, blockIdx.x + 1);
@@ -249,7 +249,7 @@ cudaError_t squares_t(const GradList& g, double* part, int* parts, cudaStream_t 
 
 template <int MAX>
 cudaError_t clip_t(const GradList& g, const double* part, int parts, float max_norm, float* norm,
-                   cudaStream_t st) {
+                   int* status, cudaStream_t st) {
   List<MAX> l;
   for (int at = 0; at < g.count;) {
     at = take(g, at, &l);
@@ -257,13 +257,15 @@ cudaError_t clip_t(const GradList& g, const double* part, int parts, float max_n
     int blocks = sm_count() * 4;
     if ((unsigned)blocks > l.pieces) blocks = (int)l.pieces;
     E2TTT_TRACE("grad_clip", st);
-    grad_clip_kernel<MAX><<<blocks, kThreads, 0, st>>>(l, part, parts, max_norm, norm);
+    grad_clip_kernel<MAX><<<blocks, kThreads, 0, st>>>(l, part, parts, max_norm, norm, status);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     norm = nullptr;  // the first launch writes it
   }
   return cudaSuccess;
 }
+
+double* partials(void* ws) { return (double*)((char*)ws + kStatusBytes); }
 
 cudaError_t squares_of(const GradList& g, double* part, int* parts, cudaStream_t st) {
   return g.count <= kFew ? squares_t<kFew>(g, part, parts, st) : squares_t<kMany>(g, part, parts, st);
@@ -272,15 +274,15 @@ cudaError_t squares_of(const GradList& g, double* part, int* parts, cudaStream_t
 }  // namespace
 
 size_t grad_workspace_bytes(int count) {
-  return (size_t)((count + kMany - 1) / kMany + 1) * kGradBlocksMax * sizeof(double);
+  return kStatusBytes + (size_t)((count + kMany - 1) / kMany + 1) * kGradBlocksMax * sizeof(double);
 }
 
 cudaError_t grad_norm(const GradList& g, float* norm, void* ws, cudaStream_t st) {
   int parts = 0;
-  const cudaError_t e = squares_of(g, (double*)ws, &parts, st);
+  const cudaError_t e = squares_of(g, partials(ws), &parts, st);
   if (e != cudaSuccess) return e;
   E2TTT_TRACE("grad_norm", st);
-  grad_norm_kernel<<<1, kThreads, 0, st>>>((const double*)ws, parts, norm);
+  grad_norm_kernel<<<1, kThreads, 0, st>>>(partials(ws), parts, norm, (int*)ws);
   return cudaGetLastError();
 }
 
@@ -289,10 +291,10 @@ cudaError_t grad_clip(const GradList& g, float max_norm, float* norm, void* ws, 
   bool any = false;
   for (int i = 0; i < g.count; ++i) any = any || g.n[i];
   if (!any) return grad_norm(g, norm, ws, st);
-  const cudaError_t e = squares_of(g, (double*)ws, &parts, st);
+  const cudaError_t e = squares_of(g, partials(ws), &parts, st);
   if (e != cudaSuccess) return e;
-  return g.count <= kFew ? clip_t<kFew>(g, (const double*)ws, parts, max_norm, norm, st)
-                         : clip_t<kMany>(g, (const double*)ws, parts, max_norm, norm, st);
+  return g.count <= kFew ? clip_t<kFew>(g, partials(ws), parts, max_norm, norm, (int*)ws, st)
+                         : clip_t<kMany>(g, partials(ws), parts, max_norm, norm, (int*)ws, st);
 }
 
 }  // namespace e2ttt

@@ -10,6 +10,9 @@
 
 namespace e2ttt {
 
+// A workspace starts with its status word (e2ttt_workspace_status), which every call resets.
+constexpr size_t kStatusBytes = 256;
+
 // Number of SMs of the current device (asked once per device and thread).
 int sm_count();
 

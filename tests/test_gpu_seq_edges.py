@@ -162,3 +162,25 @@ def test_steps_of_an_infinite_state(E):
         E.ssm_step(one, one, torch.ones(1, 1, 2, device="cuda"), torch.full((1, 1), dt, device="cuda"), S,
                    torch.tensor([-1.0], device="cuda"))
         assert S[0, 0, 0].isinf().all() and S[0, 0, 1].isfinite().all()
+
+
+def test_status_of_workspaces_without_waits(E):
+    """The convolution's gradients and the gradient norm reset the status word too,
+    whatever the workspace held: nothing of theirs can have given up."""
+    x, w = torch.randn(2, 3, 50, 12, device="cuda"), torch.randn(3, 12, 4, device="cuda")
+    grads, empty = [torch.randn(5000, device="cuda"), torch.randn(9, device="cuda")], [torch.empty(0, device="cuda")]
+    out = [torch.empty_like(t) for t in grads]
+    conv, norm = E.e2ttt_short_conv_workspace_bytes(E.make_conv_shape(2, 3, 50, 12, 4, E.F32)), E.e2ttt_grad_workspace_bytes(2)
+    for need, call in ((conv, lambda ws: E.short_conv_bwd(x, w, x, ws=ws)["dw"]),
+                       (norm, lambda ws: E.grad_norm(grads, ws=ws)),
+                       (norm, lambda ws: E.grad_norm(empty, ws=ws)),
+                       (norm, lambda ws: E.clip_grad_norm(grads, 1.0, out=out, ws=ws)),
+                       (norm, lambda ws: E.clip_grad_norm(empty, 1.0, ws=ws)),
+                       (norm, lambda ws: E.clip_grad_norm(grads * 300, 1.0, out=[t.clone() for t in grads * 300], ws=ws))):
+        if need == norm:
+            need = max(need, E.e2ttt_grad_workspace_bytes(600))
+        ws = [torch.full((need + 64,), fill, dtype=torch.uint8, device="cuda") for fill in (0xff, 0)]
+        got = [call(t[:need]) for t in ws]
+        assert all(E.e2ttt_workspace_status(t, raw=True, stream=torch.cuda.current_stream().cuda_stream) == E.OK for t in ws)
+        assert torch.equal(*got)
+        assert (ws[0][need:] == 0xff).all()  # nothing behind it

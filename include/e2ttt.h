@@ -333,9 +333,10 @@ e2ttt_status e2ttt_short_conv_step(const e2ttt_conv_shape* shape, const void* x,
  * Paths: bf16 activations with d_k <= 128 run on the tcgen05 tensor cores
  * (operands that are not inputs are rounded to bf16 where the result is bf16 and
  * enter as three bf16 terms where it is fp32; fp32 accumulation), for any
- * alignment and odd sizes; fp32 activations and larger d_k run on fp32 CUDA
- * cores. The waits of the tensor-core kernels are bounded:
- * e2ttt_workspace_status(workspace) reports one that gave up.
+ * alignment and odd sizes; fp32 activations and larger d_k run on mma.sync, with
+ * operands as pairs of tf32 values (22 bits at least) and fp32 sums. The waits of the
+ * tcgen05 kernels are bounded: e2ttt_workspace_status(workspace) reports one that gave
+ * up.
  * Limits: all sizes >= 1, H a multiple of G, d_k <= 256, d_v <= 1024,
  * B*H <= 65535, T <= 2^24, ceil(T/32)*B*H*ceil(d_v/64) < 2^31. */
 typedef struct {

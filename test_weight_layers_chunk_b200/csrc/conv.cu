@@ -14,8 +14,10 @@
 // backward the W-1 after it), which the neighbouring run has just brought into
 // L1/L2. Threads of a warp cover consecutive channels, then consecutive runs.
 // 4 x 8 heads x 2048 tokens x 256 channels, W = 4, bf16 with silu: forward 18 us
-// (67 MB), backward 31 us (101 MB), where the bytes take 10 and 16: issue-bound, with
-// two MUFU operations an element (14000 cycles of an SM's MUFU in either). Packed
+// (67 MB), backward 34 us with its sums (101 MB), where the bytes take 10 and 16; fp32:
+// 26 and 44 us, where they take 21 and 31. No unit is full (bf16: MUFU 51 and 28 % busy
+// with two operations an element, issue 45 and 44 %, DRAM 21 and 26 %): with 37 and 21 %
+// of the warps' places taken, what is left is latency that they do not cover. Packed
 // fp32 pairs, whole batches without predicates and asynchronous copies brought them
 // from 40 and 97 us; eight channels a thread needed too many registers.
 #include "seq_ops.h"
@@ -542,7 +544,7 @@ Geo geometry(const ConvDims& s, int vec, bool back) {
   // walks twice); short ones give more threads. The longest that still gives every
   // SM 768 threads, in the backward (half as many fit) 384.
   g.R = back ? 64 : 32;
-  const long long enough = 148LL * (back ? 384 : 768);
+  const long long enough = (long long)kPlannedSms * (back ? 384 : 768);
   while (g.R > 8 && (long long)s.B * s.H * g.nvec * ((s.T + g.R - 1) / g.R) < enough) g.R /= 2;
   g.runs = (s.T + g.R - 1) / g.R;
   return g;
@@ -553,7 +555,7 @@ Geo geometry(const ConvDims& s, int vec, bool back) {
 // spread over more than what fills the GPU.
 int bwd_blocks_x(const ConvDims& s, const Geo& g) {
   const int tiles = (g.runs + g.rows - 1) / g.rows;
-  const long long want = (148LL * 8 + (long long)s.B * s.H - 1) / ((long long)s.B * s.H);
+  const long long want = (kPlannedSms * 8LL + (long long)s.B * s.H - 1) / ((long long)s.B * s.H);
   return (int)(tiles < want ? tiles : want);
 }
 

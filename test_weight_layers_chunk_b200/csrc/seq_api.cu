@@ -98,7 +98,7 @@ e2ttt_status ssm_dims(const char* who, const e2ttt_ssm_shape* s, SsmDims* d) {
   d->P = s->d_v;
   d->bf16_act = s->act == E2TTT_BF16;
   d->tc = d->bf16_act && s->d_k <= 128;
-  // CUDA cores: 64 tokens to a chunk; with more than 128 state columns the
+  // mma.sync (ssm.cu): 64 tokens to a chunk; with more than 128 state columns the
   // backward's tiles of 64 tokens would not fit an SM's shared memory.
   d->Q = d->tc ? kSsmTcChunk : s->d_k <= 128 ? 64 : 32;
   d->NC = (s->T + d->Q - 1) / d->Q;

@@ -15,6 +15,9 @@ constexpr size_t kStatusBytes = 256;
 
 // Number of SMs of the current device (asked once per device and thread).
 int sm_count();
+// The SMs that work is split for where the split sets a workspace's size or the order of
+// sums: a B200's, not asked, so that both depend on the shape alone.
+constexpr int kPlannedSms = 148;
 
 // ------------------------------------------------------------------ convolution
 struct ConvDims {
@@ -43,7 +46,7 @@ struct SsmDims {
   int Q, NC;     // tokens per chunk, chunks
   int NPT;       // tiles of kSsmPT state rows
   bool bf16_act;
-  bool tc;       // chunks run on the tensor cores
+  bool tc;       // chunks run on the tcgen05 kernels (ssm_tc.cu)
 };
 constexpr int kSsmPT = 64;
 constexpr int kSsmTcChunk = 128;  // tokens per chunk on the tensor cores
@@ -63,8 +66,8 @@ struct SsmFwdArgs {
   int* status;    // device status word of the bounded waits
   cudaStream_t st;
 };
-cudaError_t ssm_fwd(const SsmFwdArgs& a);     // CUDA cores, any shape
-cudaError_t ssm_tc_fwd(const SsmFwdArgs& a);  // tensor cores, shapes with tc set
+cudaError_t ssm_fwd(const SsmFwdArgs& a);     // tf32 pairs on mma.sync, any shape
+cudaError_t ssm_tc_fwd(const SsmFwdArgs& a);  // tcgen05 kernels, shapes with tc set
 size_t ssm_tc_logs_bytes(const SsmDims& s);
 // Test hook behind e2ttt_test_stall_next_scan.
 void arm_scan_stall(int wait);

@@ -1,7 +1,12 @@
-// State-space scan in fp32 for every size and type, and the passes over chunk states that all forms share. The mathematics is in ssm.cuh.
+// State-space scan for every size and type, its single-token form, and the passes over
+// chunk states that all forms share. The mathematics is in ssm.cuh.
 //
 // A chunk's work is a handful of small matrix products from shared memory; chunks
 // meet only in their states, which one elementwise pass carries along the tokens.
+// 2 x 16 heads x 2048 tokens, 64 x 128 states, fp32: forward 196 us, backward 507; 64 x
+// 256 states in bf16: 476 and 1094 (fp32 490 and 1100: the products are the same). Bound
+// by the products' instructions: each warp splits its operands again, and q k^T is made
+// again for each head and tile of state rows.
 #include "ssm.cuh"
 #include "trace.h"
 
@@ -12,10 +17,13 @@ constexpr int kT = 256;
 
 // Products of fp32 tiles in shared memory on the warps' tensor instructions
 // (m16n8k8, tf32): each operand enters as two tf32 terms, a = a0 + a1 to 22 bits,
-// and a b = a0 b0 + a0 b1 + a1 b0 (what is left out is 2^-22 of it). Against plain
-// fp32 multiply-adds from shared memory this reads each operand value once per 16
+// and a b = a0 b0 + a0 b1 + a1 b0 (what is left out is 2^-22 of it at most). Against
+// plain fp32 multiply-adds from shared memory this reads each operand value once per 16
 // or 8 results instead of once per 4 (training step of 2 x 6 heads x 509 tokens, 48 x
-// 40 states: 99 -> 72 us).
+// 40 states: 99 -> 72 us). There, and for 8 heads x 1000 tokens of 64 x 128 states, y, S
+// and the gradients are off from 64-bit ones by 0.6 to 1.6 times what fp32 matrix
+// products of the same chunk form are (2-norms of 0.5 to 2.4e-7), dA by 2 to 3 times
+// (4 to 6e-7).
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
@@ -165,11 +173,11 @@ __global__ void __launch_bounds__(kT)
 // from `first`) or the gradients at their ends (REV 1, from the last chunk
 // back); `last` gets what is left after the last one. `copy`, where given, takes
 // them rounded to bf16 (what the outputs' products read), and without `keep` the
-// fp32 ones are not written. Elementwise along the chunks, bound by the states'
-// bytes; V is float4 where rows and pointers allow. 14 us for 16 chunks of 128 heads'
-// 64 x 128 states with only the copy written (101 MB), 31 us with both. 4 or 16
-// chunks in flight or more blocks on an SM cost up to half more on long rows: the
-// order of the accesses suffers.
+// fp32 ones are not written. Elementwise along the chunks; V is float4 where rows and
+// pointers allow. 14 to 18 us for 16 chunks of 128 heads' 64 x 128 states with only the
+// copy written (101 MB, DRAM 50 %), 31 to 35 us with both (168 MB, 28 %): bound by the
+// latency of its loads (long scoreboard, 22 % of the warps' places taken). But 4 or 16
+// chunks in flight or more blocks on an SM cost up to half more on long rows.
 __device__ __forceinline__ void store_bf16(bf16* p, float x) { *p = from_f<bf16>(x); }
 __device__ __forceinline__ void store_bf16(bf16* p, const float4& x) {
   __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
@@ -766,8 +774,8 @@ size_t cut_bwd(const SsmDims& s, char* ws, float* ddt, SsmBwdScratch* w) {
     o = up256(o + n);
     return (float*)p;
   };
-  // One part per head and state tile on CUDA cores; none where the tensor cores'
-  // only part is the result.
+  // One part per head and state tile here; none where the tcgen05 kernels' only part
+  // is the result.
   const size_t parts = s.tc ? ssm_tc_grad_parts(s) : (size_t)s.H / s.G * s.NPT;
   const size_t sums = s.tc && parts == 1 ? 0 : parts * s.B * s.G * s.T * s.N * f;
   w->status = (int*)take(256);

@@ -1213,21 +1213,23 @@ size_t grad_smem() {
 // waves of blocks, each of `fixed` + its longest stream of items, end first. `part`
 // is what one block more adds in memory traffic. All in units of an item's time.
 int item_parts(const SsmDims& s, int streams, double fixed, double part) {
-  constexpr int kSms = 148;
   const long long items = (long long)s.H / s.G * s.NPT, base = (long long)s.B * s.G * s.NC;
   int best = 1;
   double cost = 1e300;
   for (long long ns = 1; ns <= items; ++ns) {
     const long long per = (items + ns - 1) / ns;
     if ((items + per - 1) / per != ns) continue;
-    const double c = (double)((base * ns + kSms - 1) / kSms) * ((per + streams - 1) / streams + fixed) +
-                     part * ns * base / kSms;
+    const double c = (double)((base * ns + kPlannedSms - 1) / kPlannedSms) * ((per + streams - 1) / streams + fixed) +
+                     part * ns * base / kPlannedSms;
     if (c < cost) cost = c, best = (int)ns;
   }
   return best;
 }
 // The gradients: q, k and the results weigh about a third of an item; every part
-// more is one more fp32 copy of dq and dk to write and add up.
+// more is one more fp32 copy of dq and dk to write and add up. Against every other split
+// of eight shapes (8 to 64 heads in 1 to 8 groups, 300 to 16384 tokens) the forward's is
+// within 1 % of the best one, the gradients' within 9 % (13 parts where 10 were best for
+// 2 x 64 heads x 2048 tokens, 277 us against 254, and 8 where 1 was for 32 x 16384).
 int grad_parts(const SsmDims& s) { return item_parts(s, 1, 0.35, 0.04); }
 
 dim3 item_grid(const SsmDims& s, int parts, int* per) {

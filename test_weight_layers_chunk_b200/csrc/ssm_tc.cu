@@ -165,7 +165,7 @@ __device__ __forceinline__ void load8f(float (&f)[8], const float* p, int left) 
 // f as three bf16 terms that add up to it exactly (above the smallest exponents): each
 // is what the ones before leave, cut off to its first eight bits, so that it is the
 // upper half of a word as it stands. ROUND: the first term is f rounded to bf16, for a
-// product that takes it alone (cut off, it would lean towards zero by 2^-9 on average);
+// product that takes it alone (cut off, it would be 0.28 % too small on average);
 // what that leaves has at most 16 bits for the other two.
 template <bool ROUND = false>
 __device__ __forceinline__ void split3(const float (&f)[8], uint4 (&t)[3]) {
